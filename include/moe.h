@@ -34,7 +34,7 @@
  *     (a bounded spin in a kernel) records MOE_ERR_TIMEOUT in the workspace's
  *     status word, which moe_get_device_status() reads.
  *   - Results are deterministic (bitwise identical run to run).
- *   - NaN or Inf inputs: behaviour unspecified.
+ *   - NaN or Inf inputs: behaviour unspecified (the training entries say theirs).
  *
  * Dimensions (moe_dims_t): T tokens, H hidden, I expert intermediate, E
  * experts, k experts per token. Supported: T >= 1, H and I multiples of 128,
@@ -367,6 +367,98 @@ moe_status_t moe_grouped_gemm_fp4(const void* A_dev, const float* a_scales_dev, 
  * and round-to-nearest-even (ties to the even code). */
 moe_status_t moe_quantize_weight_fp4(const void* w_dev, int64_t nb, int64_t rows, int64_t cols,
                                      void* q_dev, uint8_t* s_dev, void* stream);
+
+/* ------------------------------------------------------------- training
+ * Gradients of the layer's pieces, and the update of the experts' weights.
+ * A training step runs moe_route_topk, moe_permute, moe_grouped_gemm (gu with
+ * the plain epilogue and N = 2I, or the gated one and gu again later) and
+ * moe_combine forward, and backward moe_combine_backward (dy, dw),
+ * moe_grouped_gemm_dgrad with the gated epilogue (d gu and h from dy and w2),
+ * moe_grouped_gemm_wgrad (d w2 from dy and h), moe_grouped_gemm_dgrad (d x_perm
+ * from d gu and w13), moe_grouped_gemm_wgrad (d w13 from d gu and x_perm) and
+ * moe_combine with weights of one (d x). In the gradients NaN and Inf spread as
+ * the formulas say and no further: a row of one expert never reaches another
+ * expert's results. */
+
+/* Element types of gradients. */
+typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
+
+/* Gradient of moe_grouped_gemm (bf16) with respect to its rows. For each
+ * expert e and its rows m in [offsets[e], offsets[e+1]), with
+ *   d[m, k] = sum_n dC[m, n] B[e, n, k]                               k < K:
+ *   NONE:   dA[m, k] = d[m, k]
+ *   gated (SWIGLU, GEGLU, REGLU): d is the gradient of h = act(g) * u, and
+ *           dA[m, k] = d u act'(g) (gradient of g), dA[m, K + k] = d act(g)
+ *           (gradient of u), h[m, k] = act(g) u (recomputed, for the weight
+ *           gradient of the down projection). relu'(0) = 0.
+ *   dC_dev bf16 [M_total, N]
+ *   B_dev  bf16 [E, N, K], the weights that the forward product reads
+ *   gu_dev bf16 [M_total, 2K] (gated: g, then u, per row), else NULL
+ *   dA_dev bf16 [M_total, K], gated [M_total, 2K]
+ *   h_dev  bf16 [M_total, K] or NULL (gated), else NULL
+ *   max_rows_per_expert as in moe_grouped_gemm (0 = unknown); bounds <= 64
+ *          select the small-M variant. More rows than the bound are not an error.
+ * N, K multiples of 128, E*N < 2^31. Accumulation is fp32; every output is
+ * rounded once. Offsets are clamped to [0, M_total]; rows of no expert are left
+ * as they were. Outputs overlap nothing. ws: as in moe_grouped_gemm; calls that
+ * may run at the same time need a workspace each. */
+moe_status_t moe_grouped_gemm_dgrad(const void* dC_dev, const void* B_dev, const int32_t* offsets_dev,
+                                    int32_t M_total, int32_t E, int32_t N, int32_t K,
+                                    moe_epilogue_t ep, const void* gu_dev, void* dA_dev, void* h_dev,
+                                    int32_t max_rows_per_expert, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Gradient of moe_grouped_gemm (bf16) with respect to the experts' weights:
+ *   dB[e, n, k] (+)= sum over the rows m of expert e of dC[m, n] A[m, k]
+ *   dC_dev bf16 [M_total, N], A_dev bf16 [M_total, K]
+ *   dB_dev [E, N, K] of `type`; an expert without rows gets zeros
+ *   accumulate != 0: added to what dB holds (fp32 only; an expert without rows
+ *          keeps its values)
+ * Dimensions, offsets, workspace and overlap as for moe_grouped_gemm_dgrad.
+ * Sums are fp32, in an order that does not change from run to run. */
+moe_status_t moe_grouped_gemm_wgrad(const void* dC_dev, const void* A_dev, const int32_t* offsets_dev,
+                                    int32_t M_total, int32_t E, int32_t N, int32_t K,
+                                    moe_grad_type_t type, int32_t accumulate, void* dB_dev, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* Gradient of moe_combine, out[t] = sum_j w[t, j] y_perm[inv_perm[t, j]]:
+ *   dy_perm[inv_perm[t, j]] = w[t, j] dout[t]
+ *   dw[t, j]                = sum_h dout[t, h] y_perm[inv_perm[t, j], h]
+ *   dout_dev bf16 [T, H], y_perm_dev bf16 [T*k, H], w_dev fp32 [T, k],
+ *   inv_perm_dev int32 [T, k] (a permutation of the rows, as moe_permute writes it)
+ *   dy_perm_dev bf16 [T*k, H] out; may be y_perm_dev itself
+ *   dw_dev fp32 [T, k] out (sums in fp32)
+ *   ws: NULL, or a workspace whose status word records an index outside
+ *       [0, T*k); such a slot is skipped and its dw is 0. E and I are ignored
+ *       beyond their usual limits. */
+moe_status_t moe_combine_backward(const void* dout_dev, const void* y_perm_dev, const float* w_dev,
+                                  const int32_t* inv_perm_dev, moe_dims_t d, void* dy_perm_dev,
+                                  float* dw_dev, void* ws, void* stream);
+
+/* Orthogonalised update of nb matrices (Newton-Schulz products, as the Muon
+ * optimiser makes of a momentum). For each G [rows, cols], row-major:
+ *   X = G / (|G|_F + eps);  `steps` times: A = X X^T, X = a X + (b A + c A^2) X
+ *   (for rows > cols: A = X^T X, X = a X + X (b A + c A^2));  out = scale X
+ *   g_dev   [nb, rows, cols] of g_type
+ *   out_dev bf16 [nb, rows, cols]
+ *   steps in [1, 64]; Muon's polynomial is a = 3.4445, b = -4.7750, c = 2.0315, 5 steps
+ *   ws      at least moe_orthogonalize_workspace_size(1, rows, cols) bytes;
+ *           with moe_orthogonalize_workspace_size(nb, ...) the whole stack
+ *           runs at once, with less in as many passes as it takes
+ * Any rows and cols in [1, 2^20]. The state X is fp32; the products take fp16
+ * operands (scaled so that |X|_2 about 1, which the norm and a polynomial with
+ * bounded steps give, fits) and accumulate in fp32. A polynomial that lets |X|_2
+ * grow past some hundreds gives Inf or NaN. A zero matrix gives zeros for eps >
+ * 0; NaN or Inf in one matrix do not reach another. Nothing may overlap. */
+moe_status_t moe_orthogonalize(const void* g_dev, int32_t nb, int32_t rows, int32_t cols,
+                               moe_grad_type_t g_type, int32_t steps, float a, float b, float c,
+                               float eps, float scale, void* out_dev, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Workspace bytes to run nb matrices of moe_orthogonalize at once: at most
+ * 65536 + nb (12 (rows + 127) (cols + 127) + 8 (min(rows, cols) + 127)^2). 0
+ * for invalid sizes. */
+size_t moe_orthogonalize_workspace_size(int32_t nb, int32_t rows, int32_t cols);
 
 /* moe_forward with the token rows in HOST memory: copies x_host ([T, H]
  * bf16) to the workspace, runs the layer, copies the result to out_host

@@ -31,6 +31,8 @@ __all__ = [
     "moe_grouped_gemm", "moe_combine", "moe_gather_rows", "moe_forward", "moe_forward_fp8", "moe_forward_hostio",
     "moe_quantize_act_fp8", "moe_quantize_weight_fp8", "moe_pack_weights", "moe_get_device_status",
     "moe_ep_plan_bytes", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_return",
+    "MOE_GRAD_BF16", "MOE_GRAD_F32", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "moe_combine_backward", "moe_orthogonalize", "moe_orthogonalize_workspace_size",
     "moe_clear_device_status", "moe_set_stage_events", "moe_check_wait_timeout", "EXPORTED",
 ]
 
@@ -39,6 +41,7 @@ MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = 3, 4, 5
 MOE_DTYPE_BF16, MOE_DTYPE_FP8_E4M3, MOE_DTYPE_FP8_E4M3_UE8M0, MOE_DTYPE_FP4_E2M1 = 0, 1, 2, 3
 MOE_EPILOGUE_NONE, MOE_EPILOGUE_SWIGLU, MOE_EPILOGUE_GEGLU, MOE_EPILOGUE_REGLU = 0, 1, 2, 3
 MOE_SCALE_F32, MOE_SCALE_UE8M0 = 0, 1
+MOE_GRAD_BF16, MOE_GRAD_F32 = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoe_b200.so")
@@ -62,6 +65,7 @@ class WsLayout(ctypes.Structure):
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 # C signatures: name -> (restype, argtypes)
 _SIGS = {
     "moe_last_error": (ctypes.c_char_p, []),
@@ -99,6 +103,14 @@ _SIGS = {
     "moe_ep_plan": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "moe_ep_dispatch": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp, _i64, _vp, _vp]),
     "moe_ep_return": (_i32, [_vp, _vp, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "moe_grouped_gemm_dgrad": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                      _i32, _vp, _sz, _vp]),
+    "moe_grouped_gemm_wgrad": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                      _sz, _vp]),
+    "moe_combine_backward": (_i32, [_vp, _vp, _vp, _vp, Dims, _vp, _vp, _vp, _vp]),
+    "moe_orthogonalize": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _f32, _f32, _f32,
+                                 _vp, _vp, _sz, _vp]),
+    "moe_orthogonalize_workspace_size": (_sz, [_i32, _i32, _i32]),
     "moe_get_device_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "moe_clear_device_status": (_i32, [_vp, _vp]),
     "moe_check_wait_timeout": (_i32, [_vp, _i64, _vp]),
@@ -325,6 +337,37 @@ def moe_ep_dispatch(x_perm, offsets, plan, E, G, R, row_bytes, dst_bufs, dst_row
 def moe_ep_return(y_loc, plan, E, G, cap_rows, row_bytes, src_bufs, src_rows, ws=None, stream=None):
     _check(lib().moe_ep_return(_p(y_loc), _p(plan), E, G, cap_rows, row_bytes, _p(src_bufs),
                                src_rows, _p(ws), _s(stream)))
+
+
+def moe_grouped_gemm_dgrad(dC, B, offsets, M_total, E, N, K, ep, dA, gu=None, h=None,
+                           max_rows_per_expert=0, ws=None, ws_bytes=None, stream=None):
+    _check(lib().moe_grouped_gemm_dgrad(_p(dC), _p(B), _p(offsets), M_total, E, N, K, int(ep),
+                                        _p(gu), _p(dA), _p(h), int(max_rows_per_expert), _p(ws),
+                                        _nbytes(ws, ws_bytes), _s(stream)))
+
+
+def moe_grouped_gemm_wgrad(dC, A, offsets, M_total, E, N, K, type, accumulate, dB, ws=None,
+                           ws_bytes=None, stream=None):
+    _check(lib().moe_grouped_gemm_wgrad(_p(dC), _p(A), _p(offsets), M_total, E, N, K, int(type),
+                                        int(bool(accumulate)), _p(dB), _p(ws),
+                                        _nbytes(ws, ws_bytes), _s(stream)))
+
+
+def moe_combine_backward(dout, y_perm, w, inv_perm, d, dy_perm, dw, ws=None, stream=None):
+    _check(lib().moe_combine_backward(_p(dout), _p(y_perm), _p(w), _p(inv_perm), _dims(d),
+                                      _p(dy_perm), _p(dw), _p(ws), _s(stream)))
+
+
+def moe_orthogonalize_workspace_size(nb, rows, cols) -> int:
+    return int(lib().moe_orthogonalize_workspace_size(nb, rows, cols))
+
+
+def moe_orthogonalize(g, nb, rows, cols, g_type, steps, coeffs, eps, scale, out, ws, ws_bytes=None,
+                      stream=None):
+    """coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
+    a, b, c = coeffs
+    _check(lib().moe_orthogonalize(_p(g), nb, rows, cols, int(g_type), int(steps), a, b, c, eps,
+                                   scale, _p(out), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def moe_get_device_status(ws) -> int:

@@ -4,6 +4,7 @@
 // on the host.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -84,6 +85,21 @@ cudaError_t launch_permute_noalloc(const int32_t* ids, int T, int H, int E, int 
                                    int32_t* perm_token, int32_t* inv_perm, const void* x,
                                    void* x_perm, cudaStream_t s);
 cudaError_t noalloc_status(int32_t* out, bool clear);
+
+// training (gemm_grad.cu, combine_grad.cu, orthogonalize.cu)
+cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
+                                 int E, int N, int K, int act, const void* gu, void* dA, void* h,
+                                 int32_t* status, cudaStream_t s, const char** why);
+cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
+                                 int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
+                                 cudaStream_t s, const char** why);
+cudaError_t launch_combine_backward(const void* dout, const void* y, const float* w, const int32_t* inv,
+                                    int T, int H, int k, void* dy, float* dw, int32_t* status,
+                                    cudaStream_t s);
+int64_t orthogonalize_ws_bytes(int64_t nb, int64_t rows, int64_t cols);
+cudaError_t launch_orthogonalize(const void* g, int nb, int rows, int cols, bool g_f32, int steps,
+                                 float a, float b, float c, float eps, float scale, void* out, void* ws,
+                                 size_t ws_bytes, cudaStream_t s, const char** why);
 
 static std::atomic<int64_t> g_launches{0};
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
@@ -459,6 +475,156 @@ moe_status_t moe_grouped_gemm_fp4(const void* A, const float* a_scales, const vo
                                    (int)ep, C, c_scales, at<int32_t>(ws, 0),
                                    static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "FP4 grouped GEMM: %s %s", cudaGetErrorString(e), why);
+  return ok();
+}
+
+namespace {
+
+bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uint64_t>(a), y = reinterpret_cast<uint64_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+moe_status_t check_grad_dims(int32_t M_total, int32_t E, int32_t N, int32_t K) {
+  if (M_total < 1) return fail(MOE_ERR_INVALID_ARG, "M_total must be >= 1 (got %d)", M_total);
+  if (E < 1 || E > 1024) return fail(MOE_ERR_INVALID_ARG, "E must be in [1, 1024] (got %d)", E);
+  if (N < 128 || N % 128 || K < 128 || K % 128)
+    return fail(MOE_ERR_INVALID_ARG, "N and K must be positive multiples of 128 (N=%d K=%d)", N, K);
+  if ((int64_t)E * N >= (int64_t)1 << 31)
+    return fail(MOE_ERR_INVALID_ARG, "E*N must be < 2^31 (E=%d N=%d)", E, N);
+  if (K > (1 << 24) || N > (1 << 24)) return fail(MOE_ERR_INVALID_ARG, "N and K must be <= 2^24 (N=%d K=%d)", N, K);
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t* offsets, int32_t M_total,
+                                    int32_t E, int32_t N, int32_t K, moe_epilogue_t ep, const void* gu,
+                                    void* dA, void* h, int32_t max_rows_per_expert, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_dims(M_total, E, N, K));
+  if (ep < MOE_EPILOGUE_NONE || ep > MOE_EPILOGUE_REGLU) return fail(MOE_ERR_INVALID_ARG, "bad epilogue");
+  if (max_rows_per_expert < 0)
+    return fail(MOE_ERR_INVALID_ARG, "max_rows_per_expert must be >= 0 (got %d)", max_rows_per_expert);
+  MOE_TRY(check_ptr(dC, "dC"));
+  MOE_TRY(check_ptr(B, "B"));
+  MOE_TRY(check_ptr(offsets, "expert_offsets"));
+  MOE_TRY(check_ptr(dA, "dA"));
+  MOE_TRY(check_ptr(gu, "gu", ep == MOE_EPILOGUE_NONE));
+  MOE_TRY(check_ptr(h, "h", true));
+  if (ep == MOE_EPILOGUE_NONE && (gu || h))
+    return fail(MOE_ERR_INVALID_ARG, "gu and h need a gated epilogue");
+  MOE_TRY(check_ptr(ws, "ws"));
+  if (ws_bytes < 256) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes", ws_bytes);
+  const uint64_t M = (uint64_t)M_total, out = M * K * 2 * (ep == MOE_EPILOGUE_NONE ? 1 : 2);
+  const struct { const void* p; uint64_t n; const char* name; } in[] = {
+      {dC, M * N * 2, "dC"}, {B, (uint64_t)E * N * K * 2, "B"}, {gu, M * K * 4, "gu"}, {ws, ws_bytes, "ws"}};
+  for (const auto& i : in)
+    if (overlaps(dA, out, i.p, i.n) || overlaps(h, M * K * 2, i.p, i.n))
+      return fail(MOE_ERR_INVALID_ARG, "an output overlaps %s", i.name);
+  if (overlaps(dA, out, h, M * K * 2)) return fail(MOE_ERR_INVALID_ARG, "dA and h overlap");
+  MOE_TRY(check_device());
+  const char* why = "";
+  cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h, at<int32_t>(ws, 0),
+                                       static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM row gradient: %s %s", cudaGetErrorString(e), why);
+  return ok();
+}
+
+moe_status_t moe_grouped_gemm_wgrad(const void* dC, const void* A, const int32_t* offsets, int32_t M_total,
+                                    int32_t E, int32_t N, int32_t K, moe_grad_type_t type, int32_t accumulate,
+                                    void* dB, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_dims(M_total, E, N, K));
+  if (type != MOE_GRAD_BF16 && type != MOE_GRAD_F32) return fail(MOE_ERR_INVALID_ARG, "bad gradient type");
+  if (accumulate && type != MOE_GRAD_F32)
+    return fail(MOE_ERR_INVALID_ARG, "accumulation needs an fp32 gradient (a bf16 sum would round at every call)");
+  MOE_TRY(check_ptr(dC, "dC"));
+  MOE_TRY(check_ptr(A, "A"));
+  MOE_TRY(check_ptr(offsets, "expert_offsets"));
+  MOE_TRY(check_ptr(dB, "dB"));
+  MOE_TRY(check_ptr(ws, "ws"));
+  if (ws_bytes < 256) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes", ws_bytes);
+  const uint64_t M = (uint64_t)M_total, out = (uint64_t)E * N * K * (type == MOE_GRAD_F32 ? 4 : 2);
+  if (overlaps(dB, out, dC, M * N * 2) || overlaps(dB, out, A, M * K * 2) || overlaps(dB, out, ws, ws_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "dB overlaps an input or the workspace");
+  MOE_TRY(check_device());
+  const char* why = "";
+  cudaError_t e = launch_grouped_wgrad(dC, A, offsets, M_total, E, N, K, type == MOE_GRAD_F32, accumulate != 0, dB,
+                                       at<int32_t>(ws, 0), static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM weight gradient: %s %s", cudaGetErrorString(e), why);
+  return ok();
+}
+
+moe_status_t moe_combine_backward(const void* dout, const void* y_perm, const float* w, const int32_t* inv_perm,
+                                  moe_dims_t d, void* dy_perm, float* dw, void* ws, void* stream) {
+  moe_dims_t d2 = d;
+  if (d2.I < 128) d2.I = 128;
+  MOE_TRY(check_dims(d2, true));
+  MOE_TRY(check_ptr(dout, "dout"));
+  MOE_TRY(check_ptr(y_perm, "y_perm"));
+  MOE_TRY(check_ptr(w, "topk_w"));
+  MOE_TRY(check_ptr(inv_perm, "inv_perm"));
+  MOE_TRY(check_ptr(dy_perm, "dy_perm"));
+  MOE_TRY(check_ptr(dw, "dw"));
+  MOE_TRY(check_ptr(ws, "ws", true));
+  const uint64_t R = (uint64_t)d.T * d.k, rows = R * d.H * 2, tokens = (uint64_t)d.T * d.H * 2;
+  if (dy_perm != y_perm && overlaps(dy_perm, rows, y_perm, rows))
+    return fail(MOE_ERR_INVALID_ARG, "dy_perm overlaps y_perm without being it");
+  const struct { const void* p; uint64_t n; const char* name; } in[] = {
+      {dout, tokens, "dout"}, {w, R * 4, "topk_w"}, {inv_perm, R * 4, "inv_perm"}, {ws, 4, "ws"}};
+  for (const auto& i : in)
+    if (overlaps(dy_perm, rows, i.p, i.n) || overlaps(dw, R * 4, i.p, i.n))
+      return fail(MOE_ERR_INVALID_ARG, "an output overlaps %s", i.name);
+  if (overlaps(dw, R * 4, dy_perm, rows) || overlaps(dw, R * 4, y_perm, rows))
+    return fail(MOE_ERR_INVALID_ARG, "dw overlaps y_perm or dy_perm");
+  MOE_TRY(check_device());
+  cudaError_t e = launch_combine_backward(dout, y_perm, w, inv_perm, d.T, d.H, d.k, dy_perm, dw,
+                                          static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "combine gradient");
+  return ok();
+}
+
+namespace {
+
+moe_status_t check_stack(int32_t nb, int32_t rows, int32_t cols) {
+  if (nb < 1) return fail(MOE_ERR_INVALID_ARG, "nb must be >= 1 (got %d)", nb);
+  if (rows < 1 || cols < 1 || rows > (1 << 20) || cols > (1 << 20))
+    return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^20] (got %d, %d)", rows, cols);
+  if ((int64_t)nb * (rows + 63) >= (int64_t)1 << 31)
+    return fail(MOE_ERR_INVALID_ARG, "nb * rows must be < 2^31 (nb=%d rows=%d)", nb, rows);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_orthogonalize_workspace_size(int32_t nb, int32_t rows, int32_t cols) {
+  if (check_stack(nb, rows, cols) != MOE_OK) return 0;
+  return (size_t)orthogonalize_ws_bytes(nb, rows, cols);
+}
+
+moe_status_t moe_orthogonalize(const void* g, int32_t nb, int32_t rows, int32_t cols, moe_grad_type_t g_type,
+                               int32_t steps, float a, float b, float c, float eps, float scale, void* out,
+                               void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_stack(nb, rows, cols));
+  if (g_type != MOE_GRAD_BF16 && g_type != MOE_GRAD_F32) return fail(MOE_ERR_INVALID_ARG, "bad gradient type");
+  if (steps < 1 || steps > 64) return fail(MOE_ERR_INVALID_ARG, "steps must be in [1, 64] (got %d)", steps);
+  for (float v : {a, b, c, eps, scale})
+    if (!std::isfinite(v)) return fail(MOE_ERR_INVALID_ARG, "the coefficients, eps and scale must be finite");
+  if (eps < 0.0f) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+  MOE_TRY(check_ptr(g, "g"));
+  MOE_TRY(check_ptr(out, "out"));
+  MOE_TRY(check_ptr(ws, "ws"));
+  const size_t one = (size_t)orthogonalize_ws_bytes(1, rows, cols);
+  if (ws_bytes < one)
+    return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed for one matrix", ws_bytes, one);
+  const uint64_t n = (uint64_t)nb * rows * cols, in_bytes = n * (g_type == MOE_GRAD_F32 ? 4 : 2);
+  if (overlaps(out, n * 2, g, in_bytes) || overlaps(out, n * 2, ws, ws_bytes) || overlaps(g, in_bytes, ws, ws_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "g, out and the workspace must not overlap");
+  MOE_TRY(check_device());
+  const char* why = "";
+  cudaError_t e = launch_orthogonalize(g, nb, rows, cols, g_type == MOE_GRAD_F32, steps, a, b, c, eps, scale, out, ws,
+                                       ws_bytes, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "orthogonalize: %s %s", cudaGetErrorString(e), why);
   return ok();
 }
 

@@ -1,0 +1,242 @@
+// Gradients of the grouped GEMM (moe_grouped_gemm, bf16): with respect to its
+// rows and with respect to the experts' weights. The forward computes, for the
+// rows m of expert e, C[m, n] = sum_k A[m, k] B[e, n, k]; so
+//   dA[m, k]    = sum_n dC[m, n] B[e, n, k]           (rows of e, summed over n)
+//   dB[e, n, k] = sum_{m of e} dC[m, n] A[m, k]       (summed over the rows of e)
+// Both read what the forward reads, as it is stored: in dA the weights enter
+// with their k index (the product's columns) along memory, in dB both operands
+// do, the rows being the summed axis (mm_core.cuh).
+#include <cmath>
+
+#include "mm_core.cuh"
+
+namespace moe {
+namespace mm {
+
+// ------------------------------------------------------------- row gradient
+// The gate's activation a(g) and its derivative.
+//   silu: p = 1 / (1 + e^-g), a = g p, a' = p (1 + g (1 - p))
+//   gelu: a = g Phi(g), a' = Phi(g) + g phi(g)
+//   relu: a = max(g, 0), a' = [g > 0]
+template <int ACT>
+__device__ __forceinline__ void act_grad(float g, float& a, float& da) {
+  if constexpr (ACT == kActSilu) {
+    const float p = __fdividef(1.0f, 1.0f + __expf(-g));
+    a = g * p;
+    da = p * (1.0f + g * (1.0f - p));
+  } else if constexpr (ACT == kActGelu) {
+    // erfc keeps Phi's relative accuracy for negative g, where 1 + erf cancels
+    const float p = 0.5f * erfcf(-0.7071067811865476f * g);
+    a = g * p;
+    da = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
+  } else {
+    a = fmaxf(g, 0.0f);
+    da = g > 0.0f ? 1.0f : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void load_row32(const __nv_bfloat16* src, float (&v)[32]) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 x = __ldg(s + q);
+    v[8 * q + 0] = bf16lo_to_f32(x.x);
+    v[8 * q + 1] = bf16hi_to_f32(x.x);
+    v[8 * q + 2] = bf16lo_to_f32(x.y);
+    v[8 * q + 3] = bf16hi_to_f32(x.y);
+    v[8 * q + 4] = bf16lo_to_f32(x.z);
+    v[8 * q + 5] = bf16hi_to_f32(x.z);
+    v[8 * q + 6] = bf16lo_to_f32(x.w);
+    v[8 * q + 7] = bf16hi_to_f32(x.w);
+  }
+}
+
+// Tiles of 128 rows of one expert by 256 columns, in the order of the forward's
+// 128-row GEMM: expert, band of m-tiles, n-tile, m-tile.
+// ACT: the product is the gradient d of h = a(g) u; the epilogue writes
+// dg = d u a'(g), du = d a(g) and, with h given, a(g) u.
+template <int ACT>
+struct RowGrad {
+  static constexpr bool kAMn = false, kBMn = true, kTail = false;
+  static constexpr int kBN = 256, kFmt = 1, kChunk = 0;
+  static constexpr int kSharedInts = 2 * (gg::kMaxE + 1);
+
+  const int32_t* offsets;
+  int E, M_total, N, K, NT, band;
+  const __nv_bfloat16* gu;  // [M_total, 2K]
+  __nv_bfloat16* dA;        // [M_total, K], with ACT [M_total, 2K]
+  __nv_bfloat16* h;         // [M_total, K] or nullptr
+
+  __device__ void setup(int32_t* sh) const {
+    load_offsets(offsets, E, M_total, sh + gg::kMaxE + 1);
+    ragged_tile_starts(sh + gg::kMaxE + 1, E, BM, NT, sh);
+  }
+  __device__ int total(const int32_t* sh) const { return sh[E]; }
+  __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
+    const int32_t* soff = sh + gg::kMaxE + 1;
+    const int e = gg::find_expert(sh, E, tile);
+    const int local = tile - sh[e];
+    const int mt = (soff[e + 1] - soff[e] + BM - 1) / BM;
+    const int bsz = band * NT;
+    const int b = local / bsz;
+    const int rows = min(band, mt - b * band);
+    const int l2 = local - b * bsz;
+    const int n = l2 / rows, m = b * band + l2 % rows;
+    t.a_mn = soff[e] + m * BM;
+    t.a_k = 0;
+    t.b_mn = n * kBN;
+    t.b_k = e * N;
+    t.nkb = N / BK;
+    t.tail = BK;
+    t.p[0] = soff[e + 1];
+  }
+  __device__ void epilogue(const int32_t*, const Tile& t, int, int q, int half, int lane, uint32_t taddr,
+                           unsigned char*) const {
+    const int row = t.a_mn + q * 32 + lane;
+    const bool valid = row < t.p[0];
+#pragma unroll 1
+    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2) && t.b_mn + c < K; c += 32) {
+      float d[32];
+      load_acc32(taddr + c, false, d);
+      if (!valid) continue;
+      const int col = t.b_mn + c;
+      if constexpr (ACT == kActNone) {
+        gg::store_row32(dA + (int64_t)row * K + col, d);
+      } else {
+        const __nv_bfloat16* gsrc = gu + (int64_t)row * 2 * K + col;
+        __nv_bfloat16* out = dA + (int64_t)row * 2 * K + col;
+        float g[32], u[32];
+        load_row32(gsrc, g);
+        load_row32(gsrc + K, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float a, da;
+          act_grad<ACT>(g[i], a, da);
+          g[i] = d[i] * u[i] * da;
+          d[i] *= a;
+          u[i] *= a;
+        }
+        gg::store_row32(out, g);
+        gg::store_row32(out + K, d);
+        if (h) gg::store_row32(h + (int64_t)row * K + col, u);
+      }
+    }
+  }
+};
+
+// ----------------------------------------------------------- weight gradient
+// Tiles of 128 CG by 256 of one expert's [N, K] gradient, summed over its rows.
+// Experts without rows get zeros (or are left as they are when adding).
+template <bool F32>
+struct WeightGrad {
+  static constexpr bool kAMn = true, kBMn = true, kTail = true;
+  static constexpr int kBN = 256, kFmt = 1, kChunk = 8;
+  static constexpr int kSharedInts = gg::kMaxE + 1;
+
+  const int32_t* offsets;
+  int E, M_total, N, K, mt, nt, bm;
+  bool add;
+  void* dB;
+
+  __device__ void setup(int32_t* sh) const {
+    load_offsets(offsets, E, M_total, sh);
+  }
+  __device__ int total(const int32_t*) const { return E * mt * nt; }
+  __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
+    const int e = tile / (mt * nt), l = tile - e * (mt * nt);
+    const int lo = sh[e], rows = max(sh[e + 1] - lo, 0);
+    t.a_mn = (l % mt) * bm;
+    t.b_mn = (l / mt) * kBN;
+    t.a_k = t.b_k = lo;
+    t.nkb = (rows + BK - 1) / BK;
+    t.tail = rows - (t.nkb - 1) * BK;
+    t.p[0] = e;
+  }
+  __device__ void store(const int32_t*, const Tile& t, int rank, int q, int half, int lane,
+                        const float (&d)[kBN / 2], unsigned char*) const {
+    const int n = t.a_mn + rank * BM + q * 32 + lane;
+    const int col = t.b_mn + half * (kBN / 2);
+    if (n >= N || col >= K || (F32 && add && t.nkb == 0)) return;
+    const int64_t at = ((int64_t)t.p[0] * N + n) * K + col;
+    if constexpr (F32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(dB) + at);
+#pragma unroll
+      for (int i = 0; i < kBN / 8; ++i) {
+        float4 v = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        if (add) {
+          const float4 o = dst[i];
+          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        }
+        dst[i] = v;
+      }
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dB) + at);
+#pragma unroll
+      for (int i = 0; i < kBN / 16; ++i)
+        dst[i] = make_uint4(pack_bf16x2(d[8 * i], d[8 * i + 1]), pack_bf16x2(d[8 * i + 2], d[8 * i + 3]),
+                            pack_bf16x2(d[8 * i + 4], d[8 * i + 5]), pack_bf16x2(d[8 * i + 6], d[8 * i + 7]));
+    }
+  }
+};
+
+}  // namespace mm
+
+cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
+                                 int E, int N, int K, int act, const void* gu, void* dA, void* h,
+                                 int32_t* status, cudaStream_t s, const char** why) {
+  CUtensorMap tmA, tmB;
+  if (!mm::make_operand(&tmA, dC, true, M_total, N, 128) ||
+      !mm::make_operand(&tmB, B, true, (int64_t)E * N, K, 64)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  auto go = [&](auto op) {
+    op.offsets = offsets;
+    op.E = E;
+    op.M_total = M_total;
+    op.N = N;
+    op.K = K;
+    op.NT = (int)ceil_div(K, op.kBN);
+    op.band = 16;
+    op.gu = static_cast<const __nv_bfloat16*>(gu);
+    op.dA = static_cast<__nv_bfloat16*>(dA);
+    op.h = static_cast<__nv_bfloat16*>(h);
+    const int64_t tiles = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * op.NT;
+    return mm::launch<decltype(op), 1>(tmA, tmB, op, tiles, status, s);
+  };
+  switch (act) {
+    case kActSilu: return go(mm::RowGrad<kActSilu>{});
+    case kActGelu: return go(mm::RowGrad<kActGelu>{});
+    case kActRelu: return go(mm::RowGrad<kActRelu>{});
+    default: return go(mm::RowGrad<kActNone>{});
+  }
+}
+
+cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
+                                 int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
+                                 cudaStream_t s, const char** why) {
+  CUtensorMap tmA, tmB;
+  if (!mm::make_operand(&tmA, dC, true, M_total, N, 64) ||
+      !mm::make_operand(&tmB, A, true, M_total, K, 64)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  auto go = [&](auto op, auto cg) {
+    constexpr int CG = decltype(cg)::value;
+    op.offsets = offsets;
+    op.E = E;
+    op.M_total = M_total;
+    op.N = N;
+    op.K = K;
+    op.bm = mm::BM * CG;
+    op.mt = (int)ceil_div(N, op.bm);
+    op.nt = (int)ceil_div(K, op.kBN);
+    op.add = add;
+    op.dB = dB;
+    return mm::launch<decltype(op), CG>(tmA, tmB, op, (int64_t)E * op.mt * op.nt, status, s);
+  };
+  using One = std::integral_constant<int, 1>;
+  return f32 ? go(mm::WeightGrad<true>{}, One{}) : go(mm::WeightGrad<false>{}, One{});
+}
+
+}  // namespace moe

@@ -1,0 +1,438 @@
+// The matrix-product core of the training kernels (grouped-product gradients
+// and the Newton-Schulz products): D[m, n] = sum_k A[m, k] B[n, k] per tile,
+// 16-bit operands, fp32 accumulation, tcgen05 + TMEM, operands staged by TMA.
+//
+// What the inference GEMMs do not have and these products need:
+//  * either operand may be stored with its MN index along memory (the
+//    transpose of what the forward reads): a row-major [k, mn] matrix is
+//    loaded as 128-byte-swizzled boxes of 64 mn by 64 k and handed to the MMA
+//    as an MN-major operand, so no transposed copy exists anywhere;
+//  * the summed axis may be ragged (rows of one expert): the last k block of a
+//    tile may end at any row. The rows past the end belong to the next expert
+//    or lie outside the matrix, and may hold anything, NaN included, so they
+//    are not multiplied: whole 16-row MMA steps past the end are not issued,
+//    and a warp zeroes the up to 15 rows of both operands that share the last
+//    step with valid rows, after the loads have landed and before the MMA;
+//  * CTA pairs (CG = 2): a tile is 256 x BN over two SMs, each holding 128
+//    rows of A and BN / 2 rows of B, so an SM streams 32 KB per k block instead
+//    of 48 KB for the same MMA time.
+//
+//  * sums of any length in fp32: the MMA truncates its running sum at every
+//    16-row step (measured: 1.9e-5 of the result's norm after 16397 rows, in
+//    proportion to the steps), so an Op that asks for it (kChunk) has every
+//    kChunk k blocks summed on their own and the partial sums added in
+//    registers, rounded to nearest.
+//
+// Warp roles (384 threads): 0 TMA producer, 1 TMEM allocator + MMA issuer (the
+// pair's leading CTA issues for both), 2 tail zeroing, 3 none, 4..11 epilogue
+// (TMEM lane quarter warp % 4, half of the tile's columns (warp - 4) / 4). Two
+// accumulator buffers let the epilogue of a tile or chunk overlap the next
+// one's products. Persistent: CTA (pair) c takes tiles c, c + grid, ... Every
+// wait is bounded (ptx::mbar_wait).
+//
+// An Op supplies the tiles and the epilogue:
+//   kAMn, kBMn    operand stored with MN along memory
+//   kBN           tile columns;  kFmt  1 bf16, 0 fp16
+//   kTail         tiles may end inside a k block (both operands MN-major)
+//   kChunk        k blocks summed by the MMA at a time, 0: all
+//   kSharedInts   int32 words of shared memory for its tables
+//   setup(sh)                 one warp fills the tables
+//   total(sh)                 number of tiles
+//   decode(sh, tile, Tile&)   coordinates and k range of a tile
+//   epilogue(sh, Tile, rank, quarter, half, lane, taddr, stage)  or, with kChunk,
+//   store(sh, Tile, rank, quarter, half, lane, sum, stage)
+#pragma once
+
+#include "gemm_common.cuh"
+#include "ptx_pair.cuh"
+
+namespace moe {
+namespace mm {
+
+constexpr int BM = 128;  // accumulator rows per CTA
+constexpr int BK = 64;
+constexpr int UK = 16;
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kTileA = BM * BK * 2;         // 16 KB
+constexpr int kRing = 192 * 1024;           // operand ring
+constexpr int kStageOut = 16 * 1024;        // epilogue staging, 2 KB a warp
+constexpr int kBarBytes = 512;
+constexpr int kSiteTail = 9;                // the tail-zeroing wait (status word)
+
+struct Tile {
+  int a_mn, a_k;  // A's coordinates of (row 0, k 0) of the pair's tile
+  int b_mn, b_k;
+  int nkb;        // k blocks; 0: the accumulator is zero and is not read
+  int tail;       // valid k rows of the last block (1..64)
+  int p[4];       // the Op's own
+};
+
+template <class Op, int CG>
+struct Cfg {
+  static constexpr int BN = Op::kBN;
+  static constexpr int kBRows = BN / CG;  // B rows (or columns, MN-major) in one CTA
+  static constexpr int kTileB = kBRows * BK * 2;
+  static constexpr int kStage = kTileA + kTileB;
+  static constexpr int STAGES = (kRing / kStage) > 10 ? 10 : (kRing / kStage);
+  static constexpr int kAccCols = BN < 32 ? 32 : BN;  // columns between the accumulators
+  static constexpr int kTmemCols = 2 * kAccCols;
+  static constexpr uint32_t kIdesc = ptx::make_idesc(BM * CG, BN, Op::kFmt, Op::kFmt) |
+                                     (Op::kAMn ? ptx::kIdescAMn : 0u) |
+                                     (Op::kBMn ? ptx::kIdescBMn : 0u);
+  static constexpr size_t kSmem = 1024 + (size_t)STAGES * kStage + kStageOut + kBarBytes + Op::kSharedInts * 4;
+  static_assert(kStage % 1024 == 0, "stages start on swizzle-atom boundaries");
+  static_assert(kTileB % 1024 == 0, "B tiles are whole swizzle atoms");
+  static_assert(!Op::kBMn || kBRows % 64 == 0, "MN-major boxes are 64 wide");
+  static_assert(!Op::kTail || (Op::kAMn && Op::kBMn), "a ragged sum needs rows as k");
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+// Loads MN rows [mn, mn + ROWS) by one k block of an operand into `dst`.
+template <bool MN, int ROWS, int CG>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* tm, int mn, int k,
+                                             uint32_t bar) {
+  if constexpr (MN) {
+#pragma unroll
+    for (int g = 0; g < ROWS / 64; ++g) {
+      if constexpr (CG == 2) ptx::tma_load_2d_pair(dst + g * 8192, tm, mn + 64 * g, k, bar);
+      else ptx::tma_load_2d(dst + g * 8192, tm, mn + 64 * g, k, bar);
+    }
+  } else {
+    constexpr int BOX = ROWS < 128 ? ROWS : 128;
+#pragma unroll
+    for (int g = 0; g < ROWS / BOX; ++g) {
+      if constexpr (CG == 2) ptx::tma_load_2d_pair(dst + g * BOX * 128, tm, k, mn + BOX * g, bar);
+      else ptx::tma_load_2d(dst + g * BOX * 128, tm, k, mn + BOX * g, bar);
+    }
+  }
+}
+
+// 32 accumulator columns of this thread's row, or zeros for an empty sum.
+__device__ __forceinline__ void load_acc32(uint32_t taddr, bool empty, float (&v)[32]) {
+  if (empty) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    return;
+  }
+  uint32_t r[32];
+  __syncwarp();  // the load is one instruction of the whole warp
+  ptx::tmem_ld32(taddr, r);
+  ptx::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <class Op, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ Op op, int32_t* status) {
+  using C = Cfg<Op, CG>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* stage_out = smem + STAGES * C::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_out + kStageOut);
+  // bars: full[STAGES], empty[STAGES], tail[STAGES], accf[2], acce[2], drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5);
+  int32_t* sh = reinterpret_cast<int32_t*>(stage_out + kStageOut + kBarBytes);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)ptx::cluster_ctarank() : 0;
+  const int unit0 = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const uint32_t full0 = ptx::smem_addr(bars), empty0 = full0 + STAGES * 8;
+  const uint32_t tail0 = empty0 + STAGES * 8, accf0 = tail0 + STAGES * 8, acce0 = accf0 + 16, drain = acce0 + 16;
+  // the leading CTA's barriers (this CTA's own without pairs)
+  const uint32_t lead_full0 = CG == 2 ? ptx::map_to_cta(full0, 0) : full0;
+  const uint32_t lead_acce0 = CG == 2 ? ptx::map_to_cta(acce0, 0) : acce0;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(full0 + s * 8, CG);  // one arrival a CTA, with its bytes or after its zeroing
+      ptx::mbar_init(empty0 + s * 8, 1);
+      ptx::mbar_init(tail0 + s * 8, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(accf0 + a * 8, 1);
+      ptx::mbar_init(acce0 + a * 8, kEpiWarps * CG);
+    }
+    ptx::mbar_init(drain, 1);
+    ptx::fence_barrier_init();
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(ptx::smem_addr(tmem_slot), C::kTmemCols);
+      ptx::tmem_relinquish();
+    }
+  }
+  if (warp == 2) op.setup(sh);
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) ptx::cluster_sync();  // both CTAs' barriers exist before anyone signals them
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = op.total(sh);
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t issued = 0;
+      bool ok = true;
+      for (int tile = unit0; tile < total && ok; tile += units) {
+        Tile t;
+        op.decode(sh, tile, t);
+        const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
+        for (int kb = 0; kb < t.nkb; ++kb, ++issued) {
+          const int s = (int)(issued % STAGES);
+          const uint32_t ph = (uint32_t)((issued / STAGES) & 1);
+          if (!ptx::mbar_wait(empty0 + s * 8, ph ^ 1, status, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = sbase + s * C::kStage, sb = sa + kTileA;
+          const bool zeroed = Op::kTail && kb == t.nkb - 1 && (t.tail & (UK - 1));
+          uint32_t bar;
+          if (zeroed) {  // this CTA's warp 2 waits for the bytes and arrives on `full` itself
+            bar = tail0 + s * 8;
+            ptx::mbar_arrive_expect_tx(bar, C::kStage);
+          } else {
+            bar = lead_full0 + s * 8;
+            if constexpr (CG == 2) ptx::mbar_arrive_expect_tx_cluster(bar, C::kStage);
+            else ptx::mbar_arrive_expect_tx(bar, C::kStage);
+          }
+          load_operand<Op::kAMn, BM, CG>(sa, &tmA, am, t.a_k + kb * BK, bar);
+          load_operand<Op::kBMn, C::kBRows, CG>(sb, &tmB, bn, t.b_k + kb * BK, bar);
+        }
+      }
+      if (rank == 0) gg::drain_loads<STAGES>(full0, issued, status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int64_t consumed = 0;
+      int acc = 0;
+      uint32_t acc_ph = 0;
+      bool ok = true;
+      for (int tile = unit0; tile < total && ok; tile += units) {
+        Tile t;
+        op.decode(sh, tile, t);
+        const int chunk = Op::kChunk ? Op::kChunk : t.nkb;
+        int kb = 0;
+        do {  // once without chunks; an empty sum still hands over its (unread) accumulator
+          if (!ptx::mbar_wait(acce0 + acc * 8, acc_ph ^ 1, status, kSiteMmaAccEmpty)) {
+            ok = false;
+            break;
+          }
+          if constexpr (CG == 2) ptx::fence_cluster();
+          ptx::tc_fence_after();
+          const uint32_t d = tmem_base + acc * C::kAccCols;
+          const int kb0 = kb, kb1 = min(kb + chunk, t.nkb);
+          for (; kb < kb1; ++kb, ++consumed) {
+            const int s = (int)(consumed % STAGES);
+            const uint32_t ph = (uint32_t)((consumed / STAGES) & 1);
+            if (!ptx::mbar_wait(full0 + s * 8, ph, status, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            int steps = BK / UK;
+            if (Op::kTail && kb == t.nkb - 1) {
+              steps = (t.tail + UK - 1) / UK;
+              if constexpr (CG == 2) ptx::fence_cluster();
+            }
+            ptx::tc_fence_after();
+            const uint32_t sa = sbase + s * C::kStage, sb = sa + kTileA;
+            const uint64_t da = Op::kAMn ? ptx::sw128_mnmajor_desc(sa, 8192) : ptx::sw128_kmajor_desc(sa);
+            const uint64_t db = Op::kBMn ? ptx::sw128_mnmajor_desc(sb, 8192) : ptx::sw128_kmajor_desc(sb);
+            // 16 k further: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+            constexpr uint64_t stepA = Op::kAMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+            constexpr uint64_t stepB = Op::kBMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+#pragma unroll
+            for (int kk = 0; kk < BK / UK; ++kk) {
+              if (kk < steps) {
+                const uint32_t more = kb != kb0 || kk != 0;
+                if constexpr (CG == 2) ptx::mma_f16_pair(d, da + kk * stepA, db + kk * stepB, C::kIdesc, more);
+                else ptx::mma_f16(d, da + kk * stepA, db + kk * stepB, C::kIdesc, more);
+              }
+            }
+            if constexpr (CG == 2) ptx::mma_commit_pair(empty0 + s * 8);
+            else ptx::mma_commit(empty0 + s * 8);
+          }
+          if (!ok) break;
+          if constexpr (CG == 2) ptx::mma_commit_pair(accf0 + acc * 8);
+          else ptx::mma_commit(accf0 + acc * 8);
+          acc ^= 1;
+          if (acc == 0) acc_ph ^= 1;
+        } while (kb < t.nkb);
+      }
+      // every MMA this thread issued has completed once `drain` fires
+      if constexpr (CG == 2) ptx::mma_commit_pair(drain);
+      else ptx::mma_commit(drain);
+      ptx::mbar_wait(drain, 0, status, kSiteDrain);
+    }
+  } else if (warp == 2) {
+    if constexpr (Op::kTail) {
+      int64_t stage = 0;
+      uint32_t phases = 0;  // bit s: parity of tail[s]'s next phase
+      for (int tile = unit0; tile < total; tile += units) {
+        Tile t;
+        op.decode(sh, tile, t);
+        stage += t.nkb;
+        if (t.nkb == 0 || !(t.tail & (UK - 1))) continue;
+        const int s = (int)((stage - 1) % STAGES);
+        if (!ptx::mbar_wait(tail0 + s * 8, (phases >> s) & 1u, status, kSiteTail)) break;
+        phases ^= 1u << s;
+        // rows [tail, next multiple of 16) of every 64-wide group: whole
+        // 128-byte rows, so the swizzle inside them does not matter
+        unsigned char* st = smem + s * C::kStage;
+        const int n = UK - (t.tail & (UK - 1));
+        constexpr int GROUPS = (BM + C::kBRows) / 64;
+        for (int i = lane; i < GROUPS * n * 8; i += 32) {
+          const int g = i / (n * 8), r = i - g * (n * 8);
+          *reinterpret_cast<uint4*>(st + g * 8192 + (t.tail + (r >> 3)) * 128 + (r & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) ptx::mbar_arrive_cluster(lead_full0 + s * 8);
+          else ptx::mbar_arrive(full0 + s * 8);
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    unsigned char* stage = stage_out + (warp - 4) * (kStageOut / kEpiWarps);
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    bool ok = true;
+    // waits for the next accumulator; release() gives it back
+    auto take = [&]() {
+      ok = ptx::mbar_wait(accf0 + acc * 8, acc_ph, status, kSiteEpiAccFull);
+      ptx::tc_fence_after();
+      return tmem_base + ((uint32_t)(q * 32) << 16) + acc * C::kAccCols;
+    };
+    auto release = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) ptx::mbar_arrive_cluster(lead_acce0 + acc * 8);
+        else ptx::mbar_arrive(acce0 + acc * 8);
+      }
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1;
+    };
+    for (int tile = unit0; tile < total && ok; tile += units) {
+      Tile t;
+      op.decode(sh, tile, t);
+      if constexpr (Op::kChunk != 0) {
+        constexpr int HALF = C::BN / 2;
+        float sum[HALF];
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+        for (int kb = 0; kb == 0 || kb < t.nkb; kb += Op::kChunk) {
+          const uint32_t taddr = take() + half * HALF;
+          if (!ok) break;
+          if (t.nkb != 0) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < HALF; c += 16) {
+              uint32_t v[16];
+              ptx::tmem_ld16(taddr + c, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+            }
+          }
+          release();
+        }
+        if (ok) op.store(sh, t, rank, q, half, lane, sum, stage);
+      } else {
+        const uint32_t taddr = take();
+        if (!ok) break;
+        op.epilogue(sh, t, rank, q, half, lane, taddr, stage);
+        release();
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) ptx::cluster_sync();  // no CTA leaves while the other may still signal or read it
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem_base, C::kTmemCols);
+    else ptx::tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// soff[0..E] = the experts' row offsets, clamped to [0, M_total]: an expert's
+// rows are [soff[e], soff[e + 1]), none where that is empty. Warp-wide.
+__device__ __forceinline__ void load_offsets(const int32_t* offsets, int E, int M_total, int32_t* soff) {
+  for (int e = threadIdx.x & 31; e <= E; e += 32) soff[e] = min(max(offsets[e], 0), M_total);
+  __syncwarp();
+}
+
+// tile_start[e] = number of tiles of the experts before e, each having
+// ceil(rows / rows_per_tile) * per_row_tile; tile_start[E] = their total. Warp-wide.
+__device__ __forceinline__ void ragged_tile_starts(const int32_t* soff, int E, int rows_per_tile,
+                                                   int per_row_tile, int32_t* tile_start) {
+  const int lane = threadIdx.x & 31;
+  int32_t carry = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const int rows = e < E ? max(soff[e + 1] - soff[e], 0) : 0;
+    const int32_t t = (rows + rows_per_tile - 1) / rows_per_tile * per_row_tile;
+    int32_t incl = t;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (e < E) tile_start[e] = carry + incl - t;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) tile_start[E] = carry;
+}
+
+// ------------------------------------------------------------------ host
+// A row-major [rows, cols] matrix of 16-bit elements (cols contiguous) as an
+// operand: K-major (k = cols) in boxes of 64 k by box_rows rows, or MN-major
+// (mn = cols) in boxes of 64 mn by 64 rows. Rows and columns past the matrix
+// read as zeros. `bf16` selects the element type.
+inline bool make_operand(CUtensorMap* m, const void* base, bool bf16, int64_t rows, int64_t cols,
+                         int box_rows) {
+  return make_tmap(m, base, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   2, cols, rows, box_rows);
+}
+
+template <class Op, int CG>
+inline cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const Op& op, int64_t tiles,
+                          int32_t* status, cudaStream_t s) {
+  using C = Cfg<Op, CG>;
+  auto k = mm_kernel<Op, CG>;
+  cudaError_t e = set_smem(k, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(num_sms() / CG, tiles));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, k, tmA, tmB, op, status);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace mm
+}  // namespace moe
