@@ -59,7 +59,7 @@ template <int ACT>
 struct RowGrad {
   static constexpr bool kAMn = false, kBMn = true, kTail = false;
   static constexpr int kBN = 256, kFmt = 1, kChunk = 0;
-  static constexpr int kSharedInts = 2 * (gg::kMaxE + 1);
+  static constexpr int kStageWarp = 0, kSharedInts = 2 * (gg::kMaxE + 1);
 
   const int32_t* offsets;
   int E, M_total, N, K, NT, band;
@@ -90,9 +90,9 @@ struct RowGrad {
     t.tail = BK;
     t.p[0] = soff[e + 1];
   }
-  __device__ void epilogue(const int32_t*, const Tile& t, int, int q, int half, int lane, uint32_t taddr,
-                           unsigned char*) const {
-    const int row = t.a_mn + q * 32 + lane;
+  __device__ void prefetch(const Tile&, Warp&) const {}
+  __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
+    const int row = w.row0(t.a_mn) + w.lane, half = w.half;
     const bool valid = row < t.p[0];
 #pragma unroll 1
     for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2) && t.b_mn + c < K; c += 32) {
@@ -121,22 +121,21 @@ struct RowGrad {
         if (h) gg::store_row32(h + (int64_t)row * K + col, u);
       }
     }
+    return true;
   }
 };
 
 // ----------------------------------------------------------- weight gradient
 // Tiles of 128 CG by 256 of one expert's [N, K] gradient, summed over its rows.
 // Experts without rows get zeros (or are left as they are when adding).
-template <bool F32>
+template <bool F32, bool ADD>
 struct WeightGrad {
   static constexpr bool kAMn = true, kBMn = true, kTail = true;
   static constexpr int kBN = 256, kFmt = 1, kChunk = 8;
-  static constexpr int kSharedInts = gg::kMaxE + 1;
+  static constexpr int kStageWarp = 2048, kSharedInts = gg::kMaxE + 1;
 
   const int32_t* offsets;
   int E, M_total, N, K, mt, nt, bm;
-  bool add;
-  void* dB;
 
   __device__ void setup(int32_t* sh) const {
     load_offsets(offsets, E, M_total, sh);
@@ -152,29 +151,32 @@ struct WeightGrad {
     t.tail = rows - (t.nkb - 1) * BK;
     t.p[0] = e;
   }
-  __device__ void store(const int32_t*, const Tile& t, int rank, int q, int half, int lane,
-                        const float (&d)[kBN / 2], unsigned char*) const {
-    const int n = t.a_mn + rank * BM + q * 32 + lane;
-    const int col = t.b_mn + half * (kBN / 2);
-    if (n >= N || col >= K || (F32 && add && t.nkb == 0)) return;
-    const int64_t at = ((int64_t)t.p[0] * N + n) * K + col;
-    if constexpr (F32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(dB) + at);
+  __device__ void store(const Tile& t, Warp& w, const uint32_t (&d)[kBN / 2]) const {
+    const int n = w.row0(t.a_mn), col = t.b_mn + w.half * (kBN / 2);
+    if (n >= N || col >= K || (ADD && t.nkb == 0)) return;  // all or none of the warp
+    constexpr int PER = F32 ? 16 : 32;  // columns of a box
 #pragma unroll
-      for (int i = 0; i < kBN / 8; ++i) {
-        float4 v = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-        if (add) {
-          const float4 o = dst[i];
-          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    for (int c = 0; c < kBN / 2; c += PER) {
+      w.free_boxes();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (F32) {
+          const uint32_t* v = d + c + 4 * j;
+          Warp::put(Warp::at64(w.base, w.lane, j), make_uint4(v[0], v[1], v[2], v[3]));
+        } else {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = pack_bf16x2(__uint_as_float(d[c + 8 * j + 2 * i]), __uint_as_float(d[c + 8 * j + 2 * i + 1]));
+          Warp::put(Warp::at64(w.base, w.lane, j), make_uint4(o[0], o[1], o[2], o[3]));
         }
-        dst[i] = v;
       }
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dB) + at);
-#pragma unroll
-      for (int i = 0; i < kBN / 16; ++i)
-        dst[i] = make_uint4(pack_bf16x2(d[8 * i], d[8 * i + 1]), pack_bf16x2(d[8 * i + 2], d[8 * i + 3]),
-                            pack_bf16x2(d[8 * i + 4], d[8 * i + 5]), pack_bf16x2(d[8 * i + 6], d[8 * i + 7]));
+      w.publish();
+      if (w.lane == 0) {
+        if constexpr (ADD) ptx::tma_add_3d(&w.maps->c[0], w.base, col + c, n, t.p[0]);
+        else ptx::tma_store_3d(&w.maps->c[0], w.base, col + c, n, t.p[0]);
+        ptx::bulk_commit();
+      }
     }
   }
 };
@@ -184,9 +186,9 @@ struct WeightGrad {
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
                                  int32_t* status, cudaStream_t s, const char** why) {
-  CUtensorMap tmA, tmB;
-  if (!mm::make_operand(&tmA, dC, true, M_total, N, 128) ||
-      !mm::make_operand(&tmB, B, true, (int64_t)E * N, K, 64)) {
+  mm::Maps maps = {};
+  if (!mm::make_operand(&maps.a, dC, true, M_total, N, false, mm::BM) ||
+      !mm::make_operand(&maps.b, B, true, (int64_t)E * N, K, true, 256)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -202,7 +204,7 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
     op.dA = static_cast<__nv_bfloat16*>(dA);
     op.h = static_cast<__nv_bfloat16*>(h);
     const int64_t tiles = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * op.NT;
-    return mm::launch<decltype(op), 1>(tmA, tmB, op, tiles, status, s);
+    return mm::launch<decltype(op), 1>(maps, op, tiles, status, s);
   };
   switch (act) {
     case kActSilu: return go(mm::RowGrad<kActSilu>{});
@@ -215,9 +217,13 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
 cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
                                  int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
                                  cudaStream_t s, const char** why) {
-  CUtensorMap tmA, tmB;
-  if (!mm::make_operand(&tmA, dC, true, M_total, N, 64) ||
-      !mm::make_operand(&tmB, A, true, M_total, K, 64)) {
+  mm::Maps maps = {};
+  // A pair's tile is 256 rows of dB: with N = 128 half of it would be empty.
+  const int pair = N > 128 ? 2 : 1;
+  if (!mm::make_operand(&maps.a, dC, true, M_total, N, true, mm::BM) ||
+      !mm::make_operand(&maps.b, A, true, M_total, K, true, 256 / pair) ||
+      !mm::make_boxes(&maps.c[0], dB, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      f32 ? 4 : 2, E, N, K, 64)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -231,12 +237,13 @@ cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* o
     op.bm = mm::BM * CG;
     op.mt = (int)ceil_div(N, op.bm);
     op.nt = (int)ceil_div(K, op.kBN);
-    op.add = add;
-    op.dB = dB;
-    return mm::launch<decltype(op), CG>(tmA, tmB, op, (int64_t)E * op.mt * op.nt, status, s);
+    return mm::launch<decltype(op), CG>(maps, op, (int64_t)E * op.mt * op.nt, status, s);
   };
-  using One = std::integral_constant<int, 1>;
-  return f32 ? go(mm::WeightGrad<true>{}, One{}) : go(mm::WeightGrad<false>{}, One{});
+  auto any = [&](auto op) {
+    return pair == 2 ? go(op, std::integral_constant<int, 2>{}) : go(op, std::integral_constant<int, 1>{});
+  };
+  return !f32 ? any(mm::WeightGrad<false, false>{})
+              : add ? any(mm::WeightGrad<true, true>{}) : any(mm::WeightGrad<true, false>{});
 }
 
 }  // namespace moe

@@ -35,12 +35,14 @@
 //   kBN           tile columns;  kFmt  1 bf16, 0 fp16
 //   kTail         tiles may end inside a k block (both operands MN-major)
 //   kChunk        k blocks summed by the MMA at a time, 0: all
+//   kStageWarp    bytes of staging per epilogue warp (a multiple of 1024)
 //   kSharedInts   int32 words of shared memory for its tables
 //   setup(sh)                 one warp fills the tables
 //   total(sh)                 number of tiles
 //   decode(sh, tile, Tile&)   coordinates and k range of a tile
-//   epilogue(sh, Tile, rank, quarter, half, lane, taddr, stage)  or, with kChunk,
-//   store(sh, Tile, rank, quarter, half, lane, sum, stage)
+//   prefetch(Tile, Warp&)     loads that do not need the accumulator
+//   epilogue(Tile, Warp&, taddr) -> bool  (false: a wait ran out)  or, with kChunk,
+//   store(Tile, Warp&, sum)
 #pragma once
 
 #include "gemm_common.cuh"
@@ -55,10 +57,10 @@ constexpr int UK = 16;
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTileA = BM * BK * 2;         // 16 KB
-constexpr int kRing = 192 * 1024;           // operand ring
-constexpr int kStageOut = 16 * 1024;        // epilogue staging, 2 KB a warp
+constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
-constexpr int kSiteTail = 9;                // the tail-zeroing wait (status word)
+constexpr int kSiteTail = 9;                // status word: the tail-zeroing wait,
+constexpr int kSiteLoad = 10;               // an epilogue warp's wait for its own loads
 
 struct Tile {
   int a_mn, a_k;  // A's coordinates of (row 0, k 0) of the pair's tile
@@ -74,30 +76,30 @@ struct Cfg {
   static constexpr int kBRows = BN / CG;  // B rows (or columns, MN-major) in one CTA
   static constexpr int kTileB = kBRows * BK * 2;
   static constexpr int kStage = kTileA + kTileB;
-  static constexpr int STAGES = (kRing / kStage) > 10 ? 10 : (kRing / kStage);
+  // the operand ring takes what the staging, the barriers and the tables leave
+  static constexpr int kStageOut = Op::kStageWarp * kEpiWarps;
+  static constexpr int kRest = 1024 + kStageOut + kBarBytes + Op::kSharedInts * 4;
+  static constexpr int STAGES = (kSmemMax - kRest) / kStage > 10 ? 10 : (kSmemMax - kRest) / kStage;
   static constexpr int kAccCols = BN < 32 ? 32 : BN;  // columns between the accumulators
   static constexpr int kTmemCols = 2 * kAccCols;
   static constexpr uint32_t kIdesc = ptx::make_idesc(BM * CG, BN, Op::kFmt, Op::kFmt) |
                                      (Op::kAMn ? ptx::kIdescAMn : 0u) |
                                      (Op::kBMn ? ptx::kIdescBMn : 0u);
-  static constexpr size_t kSmem = 1024 + (size_t)STAGES * kStage + kStageOut + kBarBytes + Op::kSharedInts * 4;
+  static constexpr size_t kSmem = (size_t)STAGES * kStage + kRest;
   static_assert(kStage % 1024 == 0, "stages start on swizzle-atom boundaries");
   static_assert(kTileB % 1024 == 0, "B tiles are whole swizzle atoms");
   static_assert(!Op::kBMn || kBRows % 64 == 0, "MN-major boxes are 64 wide");
   static_assert(!Op::kTail || (Op::kAMn && Op::kBMn), "a ragged sum needs rows as k");
-  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+  static_assert(STAGES >= 2, "shared memory of one CTA");
 };
 
 // Loads MN rows [mn, mn + ROWS) by one k block of an operand into `dst`.
 template <bool MN, int ROWS, int CG>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* tm, int mn, int k,
                                              uint32_t bar) {
-  if constexpr (MN) {
-#pragma unroll
-    for (int g = 0; g < ROWS / 64; ++g) {
-      if constexpr (CG == 2) ptx::tma_load_2d_pair(dst + g * 8192, tm, mn + 64 * g, k, bar);
-      else ptx::tma_load_2d(dst + g * 8192, tm, mn + 64 * g, k, bar);
-    }
+  if constexpr (MN) {  // ROWS / 64 groups of 64 mn, one box of k rows each, by one instruction
+    if constexpr (CG == 2) ptx::tma_load_3d_pair(dst, tm, 0, k, mn / 64, bar);
+    else ptx::tma_load_3d(dst, tm, 0, k, mn / 64, bar);
   } else {
     constexpr int BOX = ROWS < 128 ? ROWS : 128;
 #pragma unroll
@@ -123,27 +125,93 @@ __device__ __forceinline__ void load_acc32(uint32_t taddr, bool empty, float (&v
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+struct Maps {
+  CUtensorMap a, b;
+  CUtensorMap c[3];  // the epilogue's own
+};
+
+// An epilogue warp: which part of the tile it holds, and its staging, boxes of
+// 32 rows (lane = row) of 64 or 128 bytes, swizzled as tiled copies read and
+// write them. Staging is small on purpose: what it takes, the operand ring
+// lacks.
+struct Warp {
+  const Maps* maps;
+  int rank, q, half, lane;
+  uint32_t base;     // staging, on a 1024-byte boundary
+  uint32_t bar;      // two barriers of loads into the staging
+  uint32_t parity;   // bit i: parity of barrier i's next phase
+  uint32_t pending;  // bit i: a load is in flight on barrier i
+  int32_t* status;
+
+  // first row of this warp in a tile that starts at row m
+  __device__ __forceinline__ int row0(int m) const { return m + rank * BM + q * 32; }
+  // every store so far has read its box
+  __device__ __forceinline__ void free_boxes() const {
+    if (lane == 0) ptx::bulk_wait_read0();
+    __syncwarp();
+  }
+  // address of 16-byte piece j of row r: 64-byte rows (j < 4), 128-byte rows (j < 8)
+  static __device__ __forceinline__ uint32_t at64(uint32_t box, int r, int j) {
+    return box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
+  }
+  static __device__ __forceinline__ uint32_t at128(uint32_t box, int r, int j) {
+    return box + r * 128 + ((j ^ (r & 7)) << 4);
+  }
+  static __device__ __forceinline__ void put(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+  static __device__ __forceinline__ uint4 get(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+  }
+  // what every lane put is ready for tiled stores (by lane 0)
+  __device__ __forceinline__ void publish() const {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+  }
+  // box <- the tensor at {c0, c1, c2}; all lanes have done with the box
+  __device__ __forceinline__ void load(int i, uint32_t box, const CUtensorMap* tm, int c0, int c1, int c2,
+                                       uint32_t bytes) {
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(bar + 8 * i, bytes);
+      ptx::tma_load_3d(box, tm, c0, c1, c2, bar + 8 * i);
+    }
+    pending |= 1u << i;
+  }
+  __device__ __forceinline__ bool wait(int i) {
+    const bool ok = ptx::mbar_wait(bar + 8 * i, (parity >> i) & 1u, status, kSiteLoad);
+    parity ^= 1u << i;
+    pending &= ~(1u << i);
+    return ok;
+  }
+};
+
 template <class Op, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-    mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ Op op, int32_t* status) {
+    mm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Op op, int32_t* status) {
   using C = Cfg<Op, CG>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* stage_out = smem + STAGES * C::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_out + kStageOut);
-  // bars: full[STAGES], empty[STAGES], tail[STAGES], accf[2], acce[2], drain
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5);
-  int32_t* sh = reinterpret_cast<int32_t*>(stage_out + kStageOut + kBarBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_out + C::kStageOut);
+  // bars: full[STAGES], empty[STAGES], tail[STAGES], accf[2], acce[2], drain, load[8][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5 + 2 * kEpiWarps);
+  int32_t* sh = reinterpret_cast<int32_t*>(stage_out + C::kStageOut + kBarBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)ptx::cluster_ctarank() : 0;
   const int unit0 = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
   const uint32_t sbase = ptx::smem_addr(smem);
   const uint32_t full0 = ptx::smem_addr(bars), empty0 = full0 + STAGES * 8;
-  const uint32_t tail0 = empty0 + STAGES * 8, accf0 = tail0 + STAGES * 8, acce0 = accf0 + 16, drain = acce0 + 16;
+  const uint32_t tail0 = empty0 + STAGES * 8, accf0 = tail0 + STAGES * 8, acce0 = accf0 + 16, drain = acce0 + 16,
+                 load0 = drain + 8;
   // the leading CTA's barriers (this CTA's own without pairs)
   const uint32_t lead_full0 = CG == 2 ? ptx::map_to_cta(full0, 0) : full0;
   const uint32_t lead_acce0 = CG == 2 ? ptx::map_to_cta(acce0, 0) : acce0;
@@ -159,9 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(acce0 + a * 8, kEpiWarps * CG);
     }
     ptx::mbar_init(drain, 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) ptx::mbar_init(load0 + i * 8, 1);
     ptx::fence_barrier_init();
-    ptx::tma_prefetch_desc(&tmA);
-    ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&maps.a);
+    ptx::tma_prefetch_desc(&maps.b);
   }
   if (warp == 1) {
     if constexpr (CG == 2) {
@@ -202,11 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_arrive_expect_tx(bar, C::kStage);
           } else {
             bar = lead_full0 + s * 8;
-            if constexpr (CG == 2) ptx::mbar_arrive_expect_tx_cluster(bar, C::kStage);
-            else ptx::mbar_arrive_expect_tx(bar, C::kStage);
+            if (CG == 2 && rank != 0) ptx::mbar_arrive_expect_tx_cluster(bar, C::kStage);
+            else ptx::mbar_arrive_expect_tx(full0 + s * 8, C::kStage);
           }
-          load_operand<Op::kAMn, BM, CG>(sa, &tmA, am, t.a_k + kb * BK, bar);
-          load_operand<Op::kBMn, C::kBRows, CG>(sb, &tmB, bn, t.b_k + kb * BK, bar);
+          load_operand<Op::kAMn, BM, CG>(sa, &maps.a, am, t.a_k + kb * BK, bar);
+          load_operand<Op::kBMn, C::kBRows, CG>(sb, &maps.b, bn, t.b_k + kb * BK, bar);
         }
       }
       if (rank == 0) gg::drain_loads<STAGES>(full0, issued, status);
@@ -227,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if constexpr (CG == 2) ptx::fence_cluster();
           ptx::tc_fence_after();
           const uint32_t d = tmem_base + acc * C::kAccCols;
           const int kb0 = kb, kb1 = min(kb + chunk, t.nkb);
@@ -241,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int steps = BK / UK;
             if (Op::kTail && kb == t.nkb - 1) {
               steps = (t.tail + UK - 1) / UK;
-              if constexpr (CG == 2) ptx::fence_cluster();
-            }
+                }
             ptx::tc_fence_after();
             const uint32_t sa = sbase + s * C::kStage, sb = sa + kTileA;
             const uint64_t da = Op::kAMn ? ptx::sw128_mnmajor_desc(sa, 8192) : ptx::sw128_kmajor_desc(sa);
@@ -286,14 +353,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ptx::mbar_wait(tail0 + s * 8, (phases >> s) & 1u, status, kSiteTail)) break;
         phases ^= 1u << s;
         // rows [tail, next multiple of 16) of every 64-wide group: whole
-        // 128-byte rows, so the swizzle inside them does not matter
-        unsigned char* st = smem + s * C::kStage;
-        const int n = UK - (t.tail & (UK - 1));
+        // 128-byte rows, so the swizzle inside them does not matter. A lane
+        // holds one of the eight 16-byte pieces of every fourth group.
+        unsigned char* at = smem + s * C::kStage + (lane >> 3) * 8192 + (lane & 7) * 16;
         constexpr int GROUPS = (BM + C::kBRows) / 64;
-        for (int i = lane; i < GROUPS * n * 8; i += 32) {
-          const int g = i / (n * 8), r = i - g * (n * 8);
-          *reinterpret_cast<uint4*>(st + g * 8192 + (t.tail + (r >> 3)) * 128 + (r & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+        for (int r = t.tail; r & (UK - 1); ++r) {
+#pragma unroll
+          for (int g = 0; g < GROUPS; g += 4)
+            if (g + (lane >> 3) < GROUPS)
+              *reinterpret_cast<uint4*>(at + g * 8192 + r * 128) = make_uint4(0u, 0u, 0u, 0u);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -305,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
-    unsigned char* stage = stage_out + (warp - 4) * (kStageOut / kEpiWarps);
+    Warp w{&maps, rank, q, half, lane, ptx::smem_addr(stage_out) + (warp - 4) * Op::kStageWarp,
+           load0 + (warp - 4) * 16, 0, 0, status};
     int acc = 0;
     uint32_t acc_ph = 0;
     bool ok = true;
@@ -329,35 +398,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tile t;
       op.decode(sh, tile, t);
       if constexpr (Op::kChunk != 0) {
+        // The first (often the only) partial sum is read straight into place,
+        // all its loads in flight at once; later ones are added 16 columns at a time.
         constexpr int HALF = C::BN / 2;
-        float sum[HALF];
-#pragma unroll
-        for (int i = 0; i < HALF; ++i) sum[i] = 0.0f;
-#pragma unroll 1
-        for (int kb = 0; kb == 0 || kb < t.nkb; kb += Op::kChunk) {
+        uint32_t sum[HALF];
+        {
           const uint32_t taddr = take() + half * HALF;
           if (!ok) break;
           if (t.nkb != 0) {
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < HALF; c += 16) {
-              uint32_t v[16];
-              ptx::tmem_ld16(taddr + c, v);
-              ptx::tmem_wait_ld();
+            for (int c = 0; c < HALF; c += 32)
+              ptx::tmem_ld32(taddr + c, reinterpret_cast<uint32_t(&)[32]>(sum[c]));
+            ptx::tmem_wait_ld();
+          } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
-            }
+            for (int i = 0; i < HALF; ++i) sum[i] = 0u;
           }
           release();
         }
-        if (ok) op.store(sh, t, rank, q, half, lane, sum, stage);
+#pragma unroll 1
+        for (int kb = Op::kChunk; kb < t.nkb; kb += Op::kChunk) {
+          const uint32_t taddr = take() + half * HALF;
+          if (!ok) break;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < HALF; c += 16) {
+            uint32_t v[16];
+            ptx::tmem_ld16(taddr + c, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              sum[c + i] = __float_as_uint(__uint_as_float(sum[c + i]) + __uint_as_float(v[i]));
+          }
+          release();
+        }
+        if (ok) op.store(t, w, sum);
       } else {
+        op.prefetch(t, w);
         const uint32_t taddr = take();
         if (!ok) break;
-        op.epilogue(sh, t, rank, q, half, lane, taddr, stage);
+        ok = op.epilogue(t, w, taddr);
+        __syncwarp();
         release();
       }
     }
+    // the staging outlives the copies in and out of it
+    if (lane == 0) ptx::bulk_wait_all();
+    for (int i = 0; i < 2; ++i)
+      if (w.pending >> i & 1u) w.wait(i);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -400,25 +489,46 @@ __device__ __forceinline__ void ragged_tile_starts(const int32_t* soff, int E, i
 
 // ------------------------------------------------------------------ host
 // A row-major [rows, cols] matrix of 16-bit elements (cols contiguous) as an
-// operand: K-major (k = cols) in boxes of 64 k by box_rows rows, or MN-major
-// (mn = cols) in boxes of 64 mn by 64 rows. Rows and columns past the matrix
-// read as zeros. `bf16` selects the element type.
-inline bool make_operand(CUtensorMap* m, const void* base, bool bf16, int64_t rows, int64_t cols,
-                         int box_rows) {
-  return make_tmap(m, base, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                   2, cols, rows, box_rows);
+// operand of which a CTA holds `mn_rows` MN rows a stage: K-major (k = cols) in
+// boxes of 64 k by up to 128 rows, or MN-major (mn = cols, a multiple of 64) as
+// cols / 64 groups, in boxes of 64 mn by 64 k rows by mn_rows / 64 groups. Rows
+// and columns past the matrix read as zeros.
+inline bool make_operand(CUtensorMap* m, const void* base, bool bf16, int64_t rows, int64_t cols, bool mn_major,
+                         int mn_rows) {
+  const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!mn_major) return make_tmap(m, base, dt, 2, cols, rows, std::min(mn_rows, 128));
+  PFN_encodeTiled enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)(cols * 2), 128};
+  cuuint32_t box[3] = {64, 64, (cuuint32_t)(mn_rows / 64)}, estr[3] = {1, 1, 1};
+  return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A row-major [items, rows, cols] tensor for an
+// epilogue warp's boxes: 32 rows by row_bytes (64 or 128) of one item. Copies
+// read zeros and write nothing past an item's rows and columns.
+inline bool make_boxes(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, int64_t items,
+                       int64_t rows, int64_t cols, int row_bytes) {
+  PFN_encodeTiled enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)items};
+  cuuint64_t strides[2] = {(cuuint64_t)(cols * elem_bytes), (cuuint64_t)(rows * cols * elem_bytes)};
+  cuuint32_t box[3] = {(cuuint32_t)(row_bytes / elem_bytes), 32u, 1u}, estr[3] = {1, 1, 1};
+  return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class Op, int CG>
-inline cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const Op& op, int64_t tiles,
-                          int32_t* status, cudaStream_t s) {
+inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t* status, cudaStream_t s) {
   using C = Cfg<Op, CG>;
   auto k = mm_kernel<Op, CG>;
   cudaError_t e = set_smem(k, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(num_sms() / CG, tiles));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * CG));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -428,7 +538,9 @@ inline cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, k, tmA, tmB, op, status);
+  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(num_sms() / CG, tiles));
+  cfg.gridDim = dim3((unsigned)(units * CG));
+  e = cudaLaunchKernelEx(&cfg, k, maps, op, status);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();

@@ -34,45 +34,30 @@
 namespace moe {
 namespace mm {
 
-// One stack in flight: nb matrices. Buffers are padded to multiples of 64 in
-// both directions with zeros, which stay zero through every step.
+// One stack in flight: nb matrices. The buffers X (fp32 [nb, mp, np]), s X
+// (fp16, two of them in turn), s A and s (b A + c A^2) (fp16 [nb, pp, pp]) are
+// padded to multiples of 64 in both directions with zeros, which stay zero
+// through every step.
 struct Stack {
   int nb, rows, cols;    // the caller's matrices
   int mp, np, pp;        // padded rows, cols and min(rows, cols)
   float s, inv_s;        // the operands' scale and its inverse
   float a, b, c, scale;
   const void* g;         // [nb, rows, cols] fp32 or bf16
-  const float* inv;      // [nb] 1 / (|G|_F + eps)
-  float* x;              // [nb, mp, np] fp32, after the first step
-  __half* xh_in;         // [nb, mp, np] s X
-  __half* xh_out;
-  __half* gram;          // [nb, pp, pp] s A
-  __half* poly;          // [nb, pp, pp] s (b A + c A^2)
+  const float2* inv;     // [nb] 1 / (|G|_F + eps) as a power of two and the rest
   __nv_bfloat16* out;    // [nb, rows, cols]
-  bool first, last, g_f32, vec;  // vec: cols % 8 == 0, rows of g and out in 16-byte units
+  bool from_g, last;     // the step reads G as its state; it is the last one
+  bool vec;              // cols % 8 == 0: rows of g and out in 16-byte units
 };
-
-__device__ __forceinline__ void store_half32(__half* dst, const float (&v)[32]) {
-  uint4* d = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]);
-      o[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    d[q] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-}
 
 // The products of X with itself (POLY: of A with itself): symmetric results,
 // tiles on and above the diagonal.
 template <bool MN, bool POLY>
 struct Square {
+  static constexpr bool kPoly = POLY;
   static constexpr bool kAMn = MN, kBMn = MN, kTail = false;
   static constexpr int kBN = 256, kFmt = 0, kChunk = 0;
-  static constexpr int kSharedInts = 0;
+  static constexpr int kStageWarp = POLY ? 8192 : 4096, kSharedInts = 0;
 
   Stack st;
   int k_rows;      // rows of one matrix in the operand's map
@@ -97,51 +82,75 @@ struct Square {
     t.nkb = nkb;
     t.tail = BK;
   }
-  __device__ void epilogue(const int32_t*, const Tile& t, int rank, int q, int half, int lane, uint32_t taddr,
-                           unsigned char*) const {
-    const int row0 = t.p[1] + rank * BM + q * 32, row = row0 + lane;
-    const int pp = st.pp;
-    const int64_t base = (int64_t)t.p[0] * pp * pp;
-    __half* dst = (POLY ? st.poly : st.gram) + base;
-    const __half* gram = st.gram + base;
-    if (row0 >= pp) return;
+  // The staging's boxes of 32 x 32: the tile as it is, its mirror image, and
+  // (POLY) two that s A arrives in.
+  __device__ int steps(const Tile& t, const Warp& w) const {
+    if (w.row0(t.p[1]) >= st.pp) return 0;
+    const int left = st.pp - t.p[2] - w.half * (kBN / 2);  // columns of this half
+    return max(0, min(kBN / 2, left)) / 32;
+  }
+  __device__ void load_gram(const Tile& t, Warp& w, int i) const {
+    w.load(i & 1, w.base + 4096 + (i & 1) * 2048, &w.maps->c[1], t.p[2] + w.half * (kBN / 2) + 32 * i,
+           w.row0(t.p[1]), t.p[0], 2048);
+  }
+  __device__ void prefetch(const Tile& t, Warp& w) const {
+    if (POLY && steps(t, w) > 0) load_gram(t, w, 0);
+  }
+  __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
+    const int row0 = w.row0(t.p[1]), n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
+    const bool mirror = t.p[1] != t.p[2];  // a tile on the diagonal holds both halves itself
+    const float ci = st.c * st.inv_s;
 #pragma unroll 1
-    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2) && t.p[2] + c < pp; c += 32) {
-      const int col = t.p[2] + c;
-      if (col < row0) continue;  // below the diagonal: its mirror image is stored elsewhere
+    for (int i = 0; i < n; ++i) {
+      const int col = col0 + 32 * i;
       float v[32];
-      load_acc32(taddr + c, false, v);
+      if (POLY && i + 1 < n) load_gram(t, w, i + 1);  // its box's values were used two columns of boxes ago
+      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
       if constexpr (POLY) {
-        const float ci = st.c * st.inv_s;
-        const uint4* src = reinterpret_cast<const uint4*>(gram + (int64_t)row * pp + col);
+        if (!w.wait(i & 1)) return false;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint4 x = src[u];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const uint4 x = Warp::get(Warp::at64(w.base + 4096 + (i & 1) * 2048, w.lane, u));
+          const uint32_t p[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
             v[8 * u + 2 * j] = fmaf(st.b, f.x, ci * v[8 * u + 2 * j]);
             v[8 * u + 2 * j + 1] = fmaf(st.b, f.y, ci * v[8 * u + 2 * j + 1]);
           }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= st.inv_s;
+        for (int j = 0; j < 32; ++j) v[j] *= st.inv_s;
       }
-      if (col > row0) {
-        store_half32(dst + (int64_t)row * pp + col, v);
+      w.free_boxes();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dst[(int64_t)(col + i) * pp + row] = __float2half_rn(v[i]);
-      } else {  // the diagonal block: each element of its upper half, both ways
+      for (int u = 0; u < 4; ++u) {
+        uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const __half h = __float2half_rn(v[i]);
-          if (i >= lane) dst[(int64_t)row * pp + col + i] = h;
-          if (i > lane) dst[(int64_t)(col + i) * pp + row] = h;
+        for (int j = 0; j < 4; ++j) {
+          const __half2 h = __floats2half2_rn(v[8 * u + 2 * j], v[8 * u + 2 * j + 1]);
+          o[j] = *reinterpret_cast<const uint32_t*>(&h);
+          if (mirror) {  // element (row, col + c) goes to (col + c, row): column `lane` of the box's row c
+            const int c = 8 * u + 2 * j;
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(Warp::at64(w.base + 2048, c, w.lane >> 3) + (w.lane & 7) * 2),
+                         "h"(__half_as_ushort(h.x))
+                         : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(Warp::at64(w.base + 2048, c + 1, w.lane >> 3) + (w.lane & 7) * 2),
+                         "h"(__half_as_ushort(h.y))
+                         : "memory");
+          }
         }
+        Warp::put(Warp::at64(w.base, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      w.publish();
+      if (w.lane == 0) {
+        ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, t.p[0]);
+        if (mirror) ptx::tma_store_3d(&w.maps->c[0], w.base + 2048, row0, col, t.p[0]);
+        ptx::bulk_commit();
       }
     }
+    return true;
   }
 };
 
@@ -150,7 +159,7 @@ template <bool LEFT>
 struct Apply {
   static constexpr bool kAMn = false, kBMn = LEFT, kTail = false;
   static constexpr int kBN = 256, kFmt = 0, kChunk = 0;
-  static constexpr int kSharedInts = 0;
+  static constexpr int kStageWarp = 10 * 1024, kSharedInts = 0;
 
   Stack st;
   int nkb, bm, mt, nt;
@@ -170,85 +179,78 @@ struct Apply {
     t.nkb = nkb;
     t.tail = BK;
   }
-  __device__ void epilogue(const int32_t*, const Tile& t, int rank, int q, int half, int lane, uint32_t taddr,
-                           unsigned char*) const {
-    const int row = t.p[1] + rank * BM + q * 32 + lane;
-    const bool in = row < st.mp, real = row < st.rows;
-    const float f = st.inv_s * st.inv_s;
-    const int64_t xrow = ((int64_t)t.p[0] * st.mp + row) * st.np;
-    const int64_t grow = ((int64_t)t.p[0] * st.rows + row) * st.cols;
-    const float inv = st.first ? st.inv[t.p[0]] : 0.0f;
-#pragma unroll 1
-    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2) && t.p[2] + c < st.np; c += 32) {
-      const int col = t.p[2] + c;
-      float v[32];
-      load_acc32(taddr + c, false, v);
-      if (!in) continue;
-      // x = the old state, 0 outside the matrix
-      float x[32];
-      if (!st.first) {
-        const float4* src = reinterpret_cast<const float4*>(st.x + xrow + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 o = src[i];
-          x[4 * i] = o.x, x[4 * i + 1] = o.y, x[4 * i + 2] = o.z, x[4 * i + 3] = o.w;
-        }
-      } else {
-        load_g(grow, col, real, inv, x);
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = fmaf(st.a, x[i], f * v[i]);
-      if (!st.last) {
-        float4* dst = reinterpret_cast<float4*>(st.x + xrow + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= st.s;
-        store_half32(st.xh_out + xrow + col, v);
-      } else if (real) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= st.scale;
-        if (st.vec && col + 32 <= st.cols) {
-          gg::store_row32(st.out + grow + col, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < st.cols) st.out[grow + col + i] = __float2bfloat16_rn(v[i]);
-        }
-      }
-    }
+  // The staging: two boxes of 32 x 32 fp32, in which the old state arrives and
+  // from which the new one leaves, and one of 32 x 32 for s X or the result.
+  __device__ int steps(const Tile& t, const Warp& w) const {
+    if (w.row0(t.p[1]) >= st.mp) return 0;
+    const int left = st.np - t.p[2] - w.half * (kBN / 2);
+    return max(0, min(kBN / 2, left)) / 32;
   }
-  __device__ __forceinline__ void load_g(int64_t grow, int col, bool real, float inv, float (&x)[32]) const {
-    if (real && st.vec && col + 32 <= st.cols) {
-      if (st.g_f32) {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(st.g) + grow + col);
+  __device__ void load_state(const Tile& t, Warp& w, int i) const {
+    w.load(i & 1, w.base + (i & 1) * 4096, &w.maps->c[0], t.p[2] + w.half * (kBN / 2) + 32 * i, w.row0(t.p[1]),
+           t.p[0], 4096);
+  }
+  __device__ void prefetch(const Tile& t, Warp& w) const {
+    if (steps(t, w) == 0) return;
+    w.free_boxes();
+    load_state(t, w, 0);
+  }
+  __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
+    const int row0 = w.row0(t.p[1]), row = row0 + w.lane, n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
+    const float f = st.inv_s * st.inv_s;
+    // the first step may read G itself, the others X
+    const float2 inv = st.from_g ? st.inv[t.p[0]] : make_float2(1.0f, 1.0f);
+    const float a = st.a * inv.y;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int col = col0 + 32 * i;
+      const uint32_t box = w.base + (i & 1) * 4096, hbox = w.base + 8192;
+      w.free_boxes();
+      if (i + 1 < n) load_state(t, w, i + 1);
+      float v[32];
+      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
+      if (!w.wait(i & 1)) return false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 o = __ldg(src + i);
-          x[4 * i] = inv * o.x, x[4 * i + 1] = inv * o.y, x[4 * i + 2] = inv * o.z, x[4 * i + 3] = inv * o.w;
-        }
-      } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(st.g) + grow + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 o = __ldg(src + i);
-          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = inv * bf16lo_to_f32(w[j]);
-            x[8 * i + 2 * j + 1] = inv * bf16hi_to_f32(w[j]);
-          }
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t at = Warp::at128(box, w.lane, j);
+        const uint4 x = Warp::get(at);
+        v[4 * j] = fmaf(a, inv.x * __uint_as_float(x.x), f * v[4 * j]);
+        v[4 * j + 1] = fmaf(a, inv.x * __uint_as_float(x.y), f * v[4 * j + 1]);
+        v[4 * j + 2] = fmaf(a, inv.x * __uint_as_float(x.z), f * v[4 * j + 2]);
+        v[4 * j + 3] = fmaf(a, inv.x * __uint_as_float(x.w), f * v[4 * j + 3]);
+        if (!st.last)
+          Warp::put(at, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                   __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
       }
-      return;
-    }
+      const float s = st.last ? st.scale : st.s;
+      if (st.last && !st.vec) {  // rows of the result that a tiled store cannot address
+        if (row < st.rows) {
+          __nv_bfloat16* dst = st.out + ((int64_t)t.p[0] * st.rows + row) * st.cols + col;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      x[i] = 0.0f;
-      if (real && col + i < st.cols)
-        x[i] = inv * (st.g_f32 ? static_cast<const float*>(st.g)[grow + col + i]
-                               : __bfloat162float(static_cast<const __nv_bfloat16*>(st.g)[grow + col + i]));
+          for (int j = 0; j < 32; ++j)
+            if (col + j < st.cols) dst[j] = __float2bfloat16_rn(s * v[j]);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = s * v[8 * u + 2 * j], hi = s * v[8 * u + 2 * j + 1];
+          const __half2 h = __floats2half2_rn(lo, hi);
+          o[j] = st.last ? pack_bf16x2(lo, hi) : *reinterpret_cast<const uint32_t*>(&h);
+        }
+        Warp::put(Warp::at64(hbox, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      w.publish();
+      if (w.lane == 0) {
+        if (!st.last) ptx::tma_store_3d(&w.maps->c[1], box, col, row0, t.p[0]);
+        ptx::tma_store_3d(&w.maps->c[2], hbox, col, row0, t.p[0]);
+        ptx::bulk_commit();
+      }
     }
+    return true;
   }
 };
 
@@ -294,20 +296,26 @@ __global__ void __launch_bounds__(kNormThreads) sumsq_kernel(const T* __restrict
   if (threadIdx.x == 0) part[b * chunks + blockIdx.x] = s;
 }
 
-// xh = s G / (|G|_F + eps) in fp16, zero in the padding; inv[b] kept for the
-// first step. A block writes 32 padded rows by 64 columns... of one matrix.
+// xh = s G / (|G|_F + eps) in fp16, zero in the padding; inv[b] kept for a
+// first step that reads G as its state, else (x given) X = G / (|G|_F + eps) in
+// fp32 beside it.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const double* __restrict__ part,
-                                                                 int chunks, float eps, float* __restrict__ inv) {
+                                                                 int chunks, float eps, float2* __restrict__ inv,
+                                                                 __half* __restrict__ xh, float* __restrict__ x32) {
   const int64_t b = blockIdx.y;
   double v = 0.0;
   for (int i = threadIdx.x; i < chunks; i += kNormThreads) v += part[b * chunks + i];
-  const float r = (float)(1.0 / (sqrt(block_sum(v)) + (double)eps));
-  if (blockIdx.x == 0 && threadIdx.x == 0) inv[b] = r;
+  // 1 / (|G|_F + eps) as p r, p a power of two near 1 / |G|_F: the norm of
+  // entries near fp32's largest has an inverse below fp32's smallest normal
+  const double norm = sqrt(block_sum(v));
+  const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
+  const float p = (float)p2, r = (float)(1.0 / (norm * p2 + (double)eps * p2));
+  if (blockIdx.x == 0 && threadIdx.x == 0) inv[b] = make_float2(p, r);
   const int vpr = st.np / 8;
   const int64_t vecs = (int64_t)st.mp * vpr;
   const T* src = static_cast<const T*>(st.g) + b * st.rows * st.cols;
-  __half* dst = st.xh_in + b * st.mp * st.np;
+  const int64_t base = b * st.mp * st.np;
   for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < vecs;
        i += (int64_t)gridDim.x * kNormThreads) {
     const int row = (int)(i / vpr), col = (int)(i % vpr) * 8;
@@ -315,29 +323,36 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = 0.0f;
     if (row < st.rows) {
-      const T* p = src + (int64_t)row * st.cols + col;
+      const T* at = src + (int64_t)row * st.cols + col;
       if (st.vec && col + 8 <= st.cols) {
         if constexpr (sizeof(T) == 4) {
-          const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
+          const float4 lo = __ldg(reinterpret_cast<const float4*>(at)), hi = __ldg(reinterpret_cast<const float4*>(at) + 1);
           x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
         } else {
-          const uint4 o = __ldg(reinterpret_cast<const uint4*>(p));
+          const uint4 o = __ldg(reinterpret_cast<const uint4*>(at));
           x[0] = bf16lo_to_f32(o.x), x[1] = bf16hi_to_f32(o.x), x[2] = bf16lo_to_f32(o.y), x[3] = bf16hi_to_f32(o.y);
           x[4] = bf16lo_to_f32(o.z), x[5] = bf16hi_to_f32(o.z), x[6] = bf16lo_to_f32(o.w), x[7] = bf16hi_to_f32(o.w);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (col + j < st.cols) x[j] = (float)p[j];
+          if (col + j < st.cols) x[j] = (float)at[j];
       }
     }
     uint32_t o[4];
 #pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = p * x[j] * r;
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(x[2 * j] * r * st.s, x[2 * j + 1] * r * st.s);
+      const __half2 h = __floats2half2_rn(x[2 * j] * st.s, x[2 * j + 1] * st.s);
       o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(dst + (int64_t)row * st.np + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int64_t at = base + (int64_t)row * st.np + col;
+    *reinterpret_cast<uint4*>(xh + at) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (x32) {
+      *reinterpret_cast<float4*>(x32 + at) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(x32 + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
   }
 }
 
@@ -359,7 +374,7 @@ inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
     return o;
   };
   p.part = take(nb * p.chunks * 8);
-  p.inv = take(nb * 4);
+  p.inv = take(nb * 8);
   p.x = take(nb * p.mp * p.np * 4);
   p.xh0 = take(nb * p.mp * p.np * 2);
   p.xh1 = take(nb * p.mp * p.np * 2);
@@ -395,30 +410,31 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
   st.c = c;
   st.scale = scale;
   st.g = g;
-  st.g_f32 = g_f32;
   st.vec = cols % 8 == 0;
-  st.x = reinterpret_cast<float*>(ws + P.x);
-  st.gram = reinterpret_cast<__half*>(ws + P.gram);
-  st.poly = reinterpret_cast<__half*>(ws + P.poly);
   st.out = static_cast<__nv_bfloat16*>(out);
-  float* inv = reinterpret_cast<float*>(ws + P.inv);
+  float* x32 = reinterpret_cast<float*>(ws + P.x);
+  void* gram = ws + P.gram;
+  void* poly = ws + P.poly;
+  float2* inv = reinterpret_cast<float2*>(ws + P.inv);
   st.inv = inv;
   double* part = reinterpret_cast<double*>(ws + P.part);
   __half* xh[2] = {reinterpret_cast<__half*>(ws + P.xh0), reinterpret_cast<__half*>(ws + P.xh1)};
   int32_t* status = reinterpret_cast<int32_t*>(ws);
+  // the first step reads an fp32 G whose rows tiled loads can address itself
+  const bool g_state = g_f32 && cols % 4 == 0;
+  float* x_init = g_state ? nullptr : x32;
 
   const dim3 ngrid((unsigned)P.chunks, (unsigned)nb);
-  st.xh_in = xh[0];
   const int64_t vecs = P.mp * P.np / 8;
   const dim3 cgrid((unsigned)std::min<int64_t>(1024, ceil_div(vecs, 4 * kNormThreads)), (unsigned)nb);
   const int64_t n = (int64_t)rows * cols;
   if (g_f32) {
     sumsq_kernel<float><<<ngrid, kNormThreads, 0, s>>>(static_cast<const float*>(g), n, (int)P.chunks, part);
-    normalize_kernel<float><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv);
+    normalize_kernel<float><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv, xh[0], x_init);
   } else {
     sumsq_kernel<__nv_bfloat16><<<ngrid, kNormThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(g), n,
                                                                (int)P.chunks, part);
-    normalize_kernel<__nv_bfloat16><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv);
+    normalize_kernel<__nv_bfloat16><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv, xh[0], x_init);
   }
   note_launch();
   note_launch();
@@ -426,17 +442,24 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
   if (e != cudaSuccess) return e;
 
   const bool left = rows <= cols;
-  CUtensorMap xk[2], xmn[2], gk, pk;  // X K-major (box 128 rows) and MN-major, A and B K-major
-  bool ok = make_operand(&gk, st.gram, false, nb * P.pp, P.pp, 128) &&
-            make_operand(&pk, st.poly, false, nb * P.pp, P.pp, 128);
+  constexpr int CG = 2;
+  const CUtensorMapDataType f32t = CU_TENSOR_MAP_DATA_TYPE_FLOAT32, f16t = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap xk[2], xmn[2], gk, pk;       // operands: X K-major and MN-major, A and B K-major
+  CUtensorMap g_in, x_io, xh_out[2], g_io, p_out, o_out = {};  // the epilogues' boxes
+  bool ok = make_operand(&gk, gram, false, nb * P.pp, P.pp, false, 128) &&
+            make_operand(&pk, poly, false, nb * P.pp, P.pp, false, 128) &&
+            make_boxes(&x_io, x32, f32t, 4, nb, P.mp, P.np, 128) && make_boxes(&g_io, gram, f16t, 2, nb, P.pp, P.pp, 64) &&
+            make_boxes(&p_out, poly, f16t, 2, nb, P.pp, P.pp, 64);
   for (int i = 0; i < 2; ++i)
-    ok = ok && make_operand(&xk[i], xh[i], false, nb * P.mp, P.np, 128) &&
-         make_operand(&xmn[i], xh[i], false, nb * P.mp, P.np, 64);
+    ok = ok && make_operand(&xk[i], xh[i], false, nb * P.mp, P.np, false, 128) &&
+         make_operand(&xmn[i], xh[i], false, nb * P.mp, P.np, true, 128) &&
+         make_boxes(&xh_out[i], xh[i], f16t, 2, nb, P.mp, P.np, 64);
+  if (g_state) ok = ok && make_boxes(&g_in, g, f32t, 4, nb, rows, cols, 128);
+  if (st.vec) ok = ok && make_boxes(&o_out, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, nb, rows, cols, 64);
   if (!ok) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  constexpr int CG = 1;
   auto square = [&](auto op, const CUtensorMap& tm, int64_t k, int64_t k_rows) {
     op.st = st;
     op.k_rows = (int)k_rows;
@@ -444,27 +467,27 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
     op.bm = BM * CG;
     const int64_t mt = ceil_div(P.pp, op.bm), nt = ceil_div(P.pp, op.kBN), r = op.kBN / op.bm;
     op.tiles = (int)(r * nt * (nt + 1) / 2 - (r * nt - mt));  // the last column may lack its last tile
-    return launch<decltype(op), CG>(tm, tm, op, (int64_t)nb * op.tiles, status, s);
+    const Maps maps = {tm, tm, {op.kPoly ? p_out : g_io, g_io, g_io}};
+    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles, status, s);
   };
-  auto apply = [&](auto op, const CUtensorMap& ta, const CUtensorMap& tb) {
+  auto apply = [&](auto op, const CUtensorMap& ta, const CUtensorMap& tb, int out_buf) {
     op.st = st;
     op.nkb = (int)(P.pp / BK);
     op.bm = BM * CG;
     op.mt = (int)ceil_div(P.mp, op.bm);
     op.nt = (int)ceil_div(P.np, op.kBN);
-    return launch<decltype(op), CG>(ta, tb, op, (int64_t)nb * op.mt * op.nt, status, s);
+    const Maps maps = {ta, tb, {st.from_g ? g_in : x_io, x_io, st.last ? o_out : xh_out[out_buf]}};
+    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s);
   };
   for (int i = 0; i < steps; ++i) {
     const int in = i & 1;
-    st.xh_in = xh[in];
-    st.xh_out = xh[in ^ 1];
-    st.first = i == 0;
+    st.from_g = i == 0 && g_state;
     st.last = i == steps - 1;
     e = left ? square(Square<false, false>{}, xk[in], P.np, P.mp) : square(Square<true, false>{}, xmn[in], P.mp, P.mp);
     if (e != cudaSuccess) return e;
     e = square(Square<false, true>{}, gk, P.pp, P.pp);
     if (e != cudaSuccess) return e;
-    e = left ? apply(Apply<true>{}, pk, xmn[in]) : apply(Apply<false>{}, xk[in], pk);
+    e = left ? apply(Apply<true>{}, pk, xmn[in], in ^ 1) : apply(Apply<false>{}, xk[in], pk, in ^ 1);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

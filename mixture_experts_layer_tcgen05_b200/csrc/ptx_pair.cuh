@@ -26,17 +26,31 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
 // Instruction descriptor bits of an operand whose MN index runs along memory.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
-// Orders this thread's earlier shared-memory reads and writes (and those it
-// has observed by a barrier of the cluster) before its later ones.
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-
-// tma_store_2d that adds fp32 elements to the tensor instead of replacing
-// them (one rounding to nearest each).
-__device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src, int32_t c0, int32_t c1) {
+// 3-D tiled load of box {c0 (inner), c1, c2} into shared memory.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
   asm volatile(
-      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// tma_store_2d for a 3-D tensor.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+}
+
+// The same, adding fp32 elements to the tensor's instead of replacing them
+// (one rounding to nearest each).
+__device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
           reinterpret_cast<uint64_t>(tmap)),
-      "r"(c0), "r"(c1), "r"(src)
+      "r"(c0), "r"(c1), "r"(c2), "r"(src)
       : "memory");
 }
 
@@ -62,14 +76,21 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrive on a barrier given by its shared::cluster address.
+// Arrive on a barrier given by its shared::cluster address, handing over
+// TMEM reads that tcgen05.fence orders, or shared memory that a proxy fence
+// has given to the async proxy of its own SM. (Nothing is read through the
+// generic proxy on the other side, so there is no cluster-wide release: it
+// would wait for every outstanding access of the thread.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same, adding `bytes` to the transactions that the phase waits for.
+// Arrive, adding `bytes` to the transactions that the phase waits for. Relaxed:
+// it hands over no writes of this thread (the bytes themselves complete the
+// phase), and a release would wait for the thread's outstanding accesses at
+// every stage (measured: the pair kernels at half their rate).
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
                "r"(bytes)
                : "memory");
 }
@@ -82,6 +103,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, int32_t c2,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 

@@ -402,10 +402,11 @@ def test_orthogonalize_low_rank(shape, rank):
     check_orth(orth(G), newton64(G, 5), 5)
 
 
-@pytest.mark.parametrize("power", [-30, 0, 36])
-def test_orthogonalize_any_magnitude(power):
-    """Squares of large entries leave the fp32 range; the norm does not."""
-    G = _randn(_gen(9), 2, 100, 72, dtype=torch.float32) * 10.0**power
+@pytest.mark.parametrize("cols", [72, 71])
+@pytest.mark.parametrize("power", [-30, 0, 36, 37.9])
+def test_orthogonalize_any_magnitude(power, cols):
+    """Squares of large entries leave the fp32 range, and so may the norm and its inverse."""
+    G = (_randn(_gen(9), 2, 400, cols, dtype=torch.float32).clamp(-4, 4).double() * 10.0**power).float()
     check_orth(orth(G, eps=0.0), newton64(G, 5, eps=0.0), 5)
 
 
