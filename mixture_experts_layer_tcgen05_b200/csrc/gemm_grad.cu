@@ -131,7 +131,7 @@ struct RowGrad {
 template <bool F32, bool ADD>
 struct WeightGrad {
   static constexpr bool kAMn = true, kBMn = true, kTail = true;
-  static constexpr int kBN = 256, kFmt = 1, kChunk = 8;
+  static constexpr int kBN = 256, kFmt = 1, kChunk = F32 ? 12 : 64;
   static constexpr int kStageWarp = 2048, kSharedInts = gg::kMaxE + 1;
 
   const int32_t* offsets;

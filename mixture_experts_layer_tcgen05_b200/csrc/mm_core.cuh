@@ -125,6 +125,27 @@ __device__ __forceinline__ void load_acc32(uint32_t taddr, bool empty, float (&v
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// A position in the operand ring.
+template <int STAGES, int BYTES>
+struct Ring {
+  uint32_t stage;  // the stage's address
+  uint32_t bar;    // its barriers' offset
+  uint32_t parity = 0;
+  bool wrapped = false;
+  uint32_t base;
+  __device__ __forceinline__ explicit Ring(uint32_t b) : stage(b), bar(0), base(b) {}
+  __device__ __forceinline__ void step() {
+    stage += BYTES;
+    bar += 8;
+    if (bar == STAGES * 8) {
+      stage = base;
+      bar = 0;
+      parity ^= 1;
+      wrapped = true;
+    }
+  }
+};
+
 struct Maps {
   CUtensorMap a, b;
   CUtensorMap c[3];  // the epilogue's own
@@ -248,49 +269,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = op.total(sh);
+  // The producer's and the MMA issuer's loops run in one thread each, so a k
+  // block costs them their instructions' latencies: positions in the ring are
+  // stepped, not divided out (measured: a loop with 64-bit quotients took 675
+  // cycles a block, whatever the MMA's size; the MMAs themselves take 512).
   if (warp == 0) {
     if (lane == 0) {
-      int64_t issued = 0;
+      Ring<STAGES, C::kStage> at(sbase);
       bool ok = true;
       for (int tile = unit0; tile < total && ok; tile += units) {
         Tile t;
         op.decode(sh, tile, t);
         const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
-        for (int kb = 0; kb < t.nkb; ++kb, ++issued) {
-          const int s = (int)(issued % STAGES);
-          const uint32_t ph = (uint32_t)((issued / STAGES) & 1);
-          if (!ptx::mbar_wait(empty0 + s * 8, ph ^ 1, status, kSiteProducerEmpty)) {
+        int ka = t.a_k, kbb = t.b_k;
+        for (int left = t.nkb; left > 0; --left, ka += BK, kbb += BK) {
+          if (!ptx::mbar_wait(empty0 + at.bar, at.parity ^ 1, status, kSiteProducerEmpty)) {
             ok = false;
             break;
           }
-          const uint32_t sa = sbase + s * C::kStage, sb = sa + kTileA;
-          const bool zeroed = Op::kTail && kb == t.nkb - 1 && (t.tail & (UK - 1));
           uint32_t bar;
-          if (zeroed) {  // this CTA's warp 2 waits for the bytes and arrives on `full` itself
-            bar = tail0 + s * 8;
+          if (Op::kTail && left == 1 && (t.tail & (UK - 1))) {
+            bar = tail0 + at.bar;  // this CTA's warp 2 waits for the bytes and arrives on `full` itself
             ptx::mbar_arrive_expect_tx(bar, C::kStage);
           } else {
-            bar = lead_full0 + s * 8;
+            bar = lead_full0 + at.bar;
             if (CG == 2 && rank != 0) ptx::mbar_arrive_expect_tx_cluster(bar, C::kStage);
-            else ptx::mbar_arrive_expect_tx(full0 + s * 8, C::kStage);
+            else ptx::mbar_arrive_expect_tx(full0 + at.bar, C::kStage);
           }
-          load_operand<Op::kAMn, BM, CG>(sa, &maps.a, am, t.a_k + kb * BK, bar);
-          load_operand<Op::kBMn, C::kBRows, CG>(sb, &maps.b, bn, t.b_k + kb * BK, bar);
+          load_operand<Op::kAMn, BM, CG>(at.stage, &maps.a, am, ka, bar);
+          load_operand<Op::kBMn, C::kBRows, CG>(at.stage + kTileA, &maps.b, bn, kbb, bar);
+          at.step();
         }
       }
-      if (rank == 0) gg::drain_loads<STAGES>(full0, issued, status);
+      // every load of the ring has landed before this CTA (for a pair: both) goes
+      if (rank == 0) {
+        for (uint32_t b = 0; b < STAGES * 8; b += 8) {
+          const bool again = b < at.bar;  // used since the ring last began
+          if (again || at.wrapped) ptx::mbar_wait(full0 + b, again ? at.parity : at.parity ^ 1, status, kSiteDrain);
+        }
+      }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      int64_t consumed = 0;
+      Ring<STAGES, C::kStage> at(sbase);
       int acc = 0;
       uint32_t acc_ph = 0;
       bool ok = true;
+      // descriptors of stage 0; a stage further, 16-byte units are added
+      const uint64_t da0 = Op::kAMn ? ptx::sw128_mnmajor_desc(sbase, 8192) : ptx::sw128_kmajor_desc(sbase);
+      const uint64_t db0 = Op::kBMn ? ptx::sw128_mnmajor_desc(sbase + kTileA, 8192)
+                                    : ptx::sw128_kmajor_desc(sbase + kTileA);
+      // 16 k further: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+      constexpr uint64_t stepA = Op::kAMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+      constexpr uint64_t stepB = Op::kBMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+      auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t more) {
+        if constexpr (CG == 2) ptx::mma_f16_pair(d, da, db, C::kIdesc, more);
+        else ptx::mma_f16(d, da, db, C::kIdesc, more);
+      };
+      auto commit = [&](uint32_t bar) {
+        if constexpr (CG == 2) ptx::mma_commit_pair(bar);
+        else ptx::mma_commit(bar);
+      };
       for (int tile = unit0; tile < total && ok; tile += units) {
         Tile t;
         op.decode(sh, tile, t);
-        const int chunk = Op::kChunk ? Op::kChunk : t.nkb;
-        int kb = 0;
+        int left = t.nkb;
         do {  // once without chunks; an empty sum still hands over its (unread) accumulator
           if (!ptx::mbar_wait(acce0 + acc * 8, acc_ph ^ 1, status, kSiteMmaAccEmpty)) {
             ok = false;
@@ -298,42 +341,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::tc_fence_after();
           const uint32_t d = tmem_base + acc * C::kAccCols;
-          const int kb0 = kb, kb1 = min(kb + chunk, t.nkb);
-          for (; kb < kb1; ++kb, ++consumed) {
-            const int s = (int)(consumed % STAGES);
-            const uint32_t ph = (uint32_t)((consumed / STAGES) & 1);
-            if (!ptx::mbar_wait(full0 + s * 8, ph, status, kSiteMmaFull)) {
+          uint32_t more = 0;
+          for (int n = Op::kChunk ? min(left, Op::kChunk) : left; n > 0; --n, --left) {
+            if (!ptx::mbar_wait(full0 + at.bar, at.parity, status, kSiteMmaFull)) {
               ok = false;
               break;
             }
-            int steps = BK / UK;
-            if (Op::kTail && kb == t.nkb - 1) {
-              steps = (t.tail + UK - 1) / UK;
-                }
             ptx::tc_fence_after();
-            const uint32_t sa = sbase + s * C::kStage, sb = sa + kTileA;
-            const uint64_t da = Op::kAMn ? ptx::sw128_mnmajor_desc(sa, 8192) : ptx::sw128_kmajor_desc(sa);
-            const uint64_t db = Op::kBMn ? ptx::sw128_mnmajor_desc(sb, 8192) : ptx::sw128_kmajor_desc(sb);
-            // 16 k further: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-            constexpr uint64_t stepA = Op::kAMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
-            constexpr uint64_t stepB = Op::kBMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+            const uint32_t off = (at.stage - sbase) >> 4;
+            const uint64_t da = da0 + off, db = db0 + off;
+            if (Op::kTail && left == 1) {  // no 16-row step past the last row
+              for (int kk = 0; kk * UK < t.tail; ++kk, more = 1) mma(d, da + kk * stepA, db + kk * stepB, more);
+            } else {
+              mma(d, da, db, more);
 #pragma unroll
-            for (int kk = 0; kk < BK / UK; ++kk) {
-              if (kk < steps) {
-                const uint32_t more = kb != kb0 || kk != 0;
-                if constexpr (CG == 2) ptx::mma_f16_pair(d, da + kk * stepA, db + kk * stepB, C::kIdesc, more);
-                else ptx::mma_f16(d, da + kk * stepA, db + kk * stepB, C::kIdesc, more);
-              }
+              for (int kk = 1; kk < BK / UK; ++kk) mma(d, da + kk * stepA, db + kk * stepB, 1);
             }
-            if constexpr (CG == 2) ptx::mma_commit_pair(empty0 + s * 8);
-            else ptx::mma_commit(empty0 + s * 8);
+            more = 1;
+            commit(empty0 + at.bar);
+            at.step();
           }
           if (!ok) break;
-          if constexpr (CG == 2) ptx::mma_commit_pair(accf0 + acc * 8);
-          else ptx::mma_commit(accf0 + acc * 8);
+          commit(accf0 + acc * 8);
           acc ^= 1;
           if (acc == 0) acc_ph ^= 1;
-        } while (kb < t.nkb);
+        } while (left > 0);
       }
       // every MMA this thread issued has completed once `drain` fires
       if constexpr (CG == 2) ptx::mma_commit_pair(drain);
@@ -342,14 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     if constexpr (Op::kTail) {
-      int64_t stage = 0;
+      int slot = 0;         // stage of the tile's first k block
       uint32_t phases = 0;  // bit s: parity of tail[s]'s next phase
       for (int tile = unit0; tile < total; tile += units) {
         Tile t;
         op.decode(sh, tile, t);
-        stage += t.nkb;
+        const int s = (slot + t.nkb + STAGES - 1) % STAGES;  // of its last one
+        slot = (slot + t.nkb) % STAGES;
         if (t.nkb == 0 || !(t.tail & (UK - 1))) continue;
-        const int s = (int)((stage - 1) % STAGES);
         if (!ptx::mbar_wait(tail0 + s * 8, (phases >> s) & 1u, status, kSiteTail)) break;
         phases ^= 1u << s;
         // rows [tail, next multiple of 16) of every 64-wide group: whole
