@@ -262,11 +262,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_relinquish();
     }
   }
-  if (warp == 2) op.setup(sh);
+  if (warp == 2) {
+    ptx::wait_for_previous_grid();
+    op.setup(sh);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) ptx::cluster_sync();  // both CTAs' barriers exist before anyone signals them
   ptx::tc_fence_after();
+  ptx::let_next_grid_start();
+  ptx::wait_for_previous_grid();
   const uint32_t tmem_base = *tmem_slot;
   const int total = op.total(sh);
   // The producer's and the MMA issuer's loops run in one thread each, so a k
@@ -554,8 +559,11 @@ inline bool make_boxes(CUtensorMap* m, const void* base, CUtensorMapDataType dt,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// overlap: the kernel may start (its set-up, up to wait_for_previous_grid)
+// while the one ahead of it in the stream still runs.
 template <class Op, int CG>
-inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t* status, cudaStream_t s) {
+inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t* status, cudaStream_t s,
+                          bool overlap = false) {
   using C = Cfg<Op, CG>;
   auto k = mm_kernel<Op, CG>;
   cudaError_t e = set_smem(k, C::kSmem);
@@ -564,15 +572,40 @@ inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2] = {};
   cfg.attrs = at;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  if (CG == 2) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = CG;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (overlap) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   const int64_t units = std::max<int64_t>(1, std::min<int64_t>(num_sms() / CG, tiles));
   cfg.gridDim = dim3((unsigned)(units * CG));
   e = cudaLaunchKernelEx(&cfg, k, maps, op, status);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
+// A plain kernel that starts with wait_for_previous_grid, launched to overlap.
+template <typename... Par, typename... Arg>
+inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned threads, cudaStream_t s, Arg... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k, static_cast<Par>(args)...);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();

@@ -275,6 +275,8 @@ __device__ __forceinline__ double block_sum(double v) {
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) sumsq_kernel(const T* __restrict__ g, int64_t n, int chunks,
                                                              double* __restrict__ part) {
+  ptx::let_next_grid_start();
+  ptx::wait_for_previous_grid();
   const int64_t b = blockIdx.y;
   const int64_t per = (n + chunks - 1) / chunks, lo = per * blockIdx.x, hi = min(lo + per, n);
   const T* src = g + b * n;
@@ -303,6 +305,8 @@ template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const double* __restrict__ part,
                                                                  int chunks, float eps, float2* __restrict__ inv,
                                                                  __half* __restrict__ xh, float* __restrict__ x32) {
+  ptx::let_next_grid_start();
+  ptx::wait_for_previous_grid();
   const int64_t b = blockIdx.y;
   double v = 0.0;
   for (int i = threadIdx.x; i < chunks; i += kNormThreads) v += part[b * chunks + i];
@@ -428,17 +432,16 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
   const int64_t vecs = P.mp * P.np / 8;
   const dim3 cgrid((unsigned)std::min<int64_t>(1024, ceil_div(vecs, 4 * kNormThreads)), (unsigned)nb);
   const int64_t n = (int64_t)rows * cols;
-  if (g_f32) {
-    sumsq_kernel<float><<<ngrid, kNormThreads, 0, s>>>(static_cast<const float*>(g), n, (int)P.chunks, part);
-    normalize_kernel<float><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv, xh[0], x_init);
-  } else {
-    sumsq_kernel<__nv_bfloat16><<<ngrid, kNormThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(g), n,
-                                                               (int)P.chunks, part);
-    normalize_kernel<__nv_bfloat16><<<cgrid, kNormThreads, 0, s>>>(st, part, (int)P.chunks, eps, inv, xh[0], x_init);
-  }
-  note_launch();
-  note_launch();
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  auto norms = [&](auto zero) {
+    using T = decltype(zero);
+    e = launch_overlapped(sumsq_kernel<T>, ngrid, kNormThreads, s, static_cast<const T*>(g), n, (int)P.chunks, part);
+    if (e == cudaSuccess)
+      e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, st, (const double*)part, (int)P.chunks, eps,
+                            inv, xh[0], x_init);
+  };
+  if (g_f32) norms(0.0f);
+  else norms(__nv_bfloat16());
   if (e != cudaSuccess) return e;
 
   const bool left = rows <= cols;
@@ -468,7 +471,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
     const int64_t mt = ceil_div(P.pp, op.bm), nt = ceil_div(P.pp, op.kBN), r = op.kBN / op.bm;
     op.tiles = (int)(r * nt * (nt + 1) / 2 - (r * nt - mt));  // the last column may lack its last tile
     const Maps maps = {tm, tm, {op.kPoly ? p_out : g_io, g_io, g_io}};
-    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles, status, s);
+    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles, status, s, true);
   };
   auto apply = [&](auto op, const CUtensorMap& ta, const CUtensorMap& tb, int out_buf) {
     op.st = st;
@@ -477,7 +480,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
     op.mt = (int)ceil_div(P.mp, op.bm);
     op.nt = (int)ceil_div(P.np, op.kBN);
     const Maps maps = {ta, tb, {st.from_g ? g_in : x_io, x_io, st.last ? o_out : xh_out[out_buf]}};
-    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s);
+    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s, true);
   };
   for (int i = 0; i < steps; ++i) {
     const int in = i & 1;

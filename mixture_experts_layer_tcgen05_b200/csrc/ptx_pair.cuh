@@ -54,6 +54,15 @@ __device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32
       : "memory");
 }
 
+// A kernel launched with programmatic stream serialisation may start before
+// the one ahead of it in its stream has ended; until this returns, nothing that
+// kernel writes may be read, and nothing it reads written. (Returns at once in
+// a kernel launched without.)
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream start, if it was launched that way, once
+// every CTA has said so (or ended).
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------- CTA pairs (clusters of 2)
 // In a pair, the even CTA leads: it issues the MMAs of both (M = 256, each
 // CTA's shared memory holding its 128 rows of A and its half of B's rows,
