@@ -45,6 +45,8 @@
 //   store(Tile, Warp&, sum)
 #pragma once
 
+#include <atomic>
+
 #include "gemm_common.cuh"
 #include "ptx_pair.cuh"
 
@@ -566,8 +568,17 @@ inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t
                           bool overlap = false) {
   using C = Cfg<Op, CG>;
   auto k = mm_kernel<Op, CG>;
-  cudaError_t e = set_smem(k, C::kSmem);
+  // once per device: a fifth of a launch's host time
+  static std::atomic<uint64_t> sized{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(sized.load(std::memory_order_relaxed) & bit)) {
+    e = set_smem(k, C::kSmem);
+    if (e != cudaSuccess) return e;
+    sized.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;

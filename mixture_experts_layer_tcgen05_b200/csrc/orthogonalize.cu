@@ -50,40 +50,52 @@ struct Stack {
   bool vec;              // cols % 8 == 0: rows of g and out in 16-byte units
 };
 
-// The products of X with itself (POLY: of A with itself): symmetric results,
-// tiles on and above the diagonal.
-template <bool MN, bool POLY>
+// The products of X with itself (kGram, kPart) or of A with itself (kPoly):
+// symmetric results, tiles on and above the diagonal.
+// kPart: a tile's sum over k is cut into `parts` ranges that run as tiles of
+// their own and leave their fp32 sums in [part, matrix, pp, pp]; sum_parts_kernel
+// adds them. One narrow matrix has too few tiles for the GPU otherwise (measured:
+// 7168 x 256, one tile, A in 43 us against 11 in 28 parts with their sum).
+enum SquareMode { kGram, kPart, kPoly };
+template <bool MN, SquareMode MODE, int SIDE>
 struct Square {
-  static constexpr bool kPoly = POLY;
+  static constexpr bool POLY = MODE == kPoly;
   static constexpr bool kAMn = MN, kBMn = MN, kTail = false;
-  static constexpr int kBN = 256, kFmt = 0, kChunk = 0;
+  static constexpr int kBN = SIDE, kFmt = 0, kChunk = 0;
   static constexpr int kStageWarp = POLY ? 8192 : 4096, kSharedInts = 0;
 
   Stack st;
-  int k_rows;      // rows of one matrix in the operand's map
-  int nkb, bm, tiles;  // tiles of one matrix
+  int k_rows;          // rows of one matrix in the operand's map
+  int nkb, tiles;      // k blocks and tiles of one matrix
+  int parts;           // kPart: ranges of k
 
   __device__ void setup(int32_t*) const {}
-  __device__ int total(const int32_t*) const { return st.nb * tiles; }
+  __device__ int total(const int32_t*) const { return st.nb * tiles * (MODE == kPart ? parts : 1); }
   __device__ void decode(const int32_t*, int tile, Tile& t) const {
+    int kb0 = 0, kb1 = nkb, part = 0;
+    if constexpr (MODE == kPart) {
+      part = tile % parts;
+      tile /= parts;
+      kb0 = (int)((int64_t)nkb * part / parts);
+      kb1 = (int)((int64_t)nkb * (part + 1) / parts);
+    }
     const int b = tile / tiles, l = tile - b * tiles;
-    // column j of tiles holds (j + 1) r of them, r = 256 / bm
-    const int r = kBN / bm;
-    int j = (int)((sqrtf(1.0f + 8.0f * (float)l / (float)r) - 1.0f) * 0.5f);
-    while (r * j * (j + 1) / 2 > l) --j;
-    while (r * (j + 1) * (j + 2) / 2 <= l) ++j;
-    const int i = l - r * j * (j + 1) / 2;
-    t.p[0] = b;
-    t.p[1] = i * bm;
-    t.p[2] = j * kBN;
-    t.a_mn = i * bm + (MN ? 0 : b * k_rows);
-    t.b_mn = j * kBN + (MN ? 0 : b * k_rows);
-    t.a_k = t.b_k = MN ? b * k_rows : 0;
-    t.nkb = nkb;
+    // column j of tiles holds j + 1 of them
+    int j = (int)((sqrtf(1.0f + 8.0f * (float)l) - 1.0f) * 0.5f);
+    while (j * (j + 1) / 2 > l) --j;
+    while ((j + 1) * (j + 2) / 2 <= l) ++j;
+    const int i = l - j * (j + 1) / 2;
+    t.p[0] = MODE == kPart ? part * st.nb + b : b;  // the item written
+    t.p[1] = i * SIDE;
+    t.p[2] = j * SIDE;
+    t.a_mn = i * SIDE + (MN ? 0 : b * k_rows);
+    t.b_mn = j * SIDE + (MN ? 0 : b * k_rows);
+    t.a_k = t.b_k = (MN ? b * k_rows : 0) + kb0 * BK;
+    t.nkb = kb1 - kb0;
     t.tail = BK;
   }
   // The staging's boxes of 32 x 32: the tile as it is, its mirror image, and
-  // (POLY) two that s A arrives in.
+  // (kPoly) two that s A arrives in; kPart: one box of 32 x 32 fp32.
   __device__ int steps(const Tile& t, const Warp& w) const {
     if (w.row0(t.p[1]) >= st.pp) return 0;
     const int left = st.pp - t.p[2] - w.half * (kBN / 2);  // columns of this half
@@ -119,6 +131,19 @@ struct Square {
             v[8 * u + 2 * j + 1] = fmaf(st.b, f.y, ci * v[8 * u + 2 * j + 1]);
           }
         }
+      } else if constexpr (MODE == kPart) {
+        w.free_boxes();
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          Warp::put(Warp::at128(w.base, w.lane, u),
+                    make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
+                               __float_as_uint(v[4 * u + 3])));
+        w.publish();
+        if (w.lane == 0) {
+          ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, t.p[0]);
+          ptx::bulk_commit();
+        }
+        continue;
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] *= st.inv_s;
@@ -155,20 +180,20 @@ struct Square {
 };
 
 // X <- a X + B X (LEFT) or a X + X B.
-template <bool LEFT>
+template <bool LEFT, int SIDE>
 struct Apply {
   static constexpr bool kAMn = false, kBMn = LEFT, kTail = false;
-  static constexpr int kBN = 256, kFmt = 0, kChunk = 0;
+  static constexpr int kBN = SIDE, kFmt = 0, kChunk = 0;
   static constexpr int kStageWarp = 10 * 1024, kSharedInts = 0;
 
   Stack st;
-  int nkb, bm, mt, nt;
+  int nkb, mt, nt;
 
   __device__ void setup(int32_t*) const {}
   __device__ int total(const int32_t*) const { return st.nb * mt * nt; }
   __device__ void decode(const int32_t*, int tile, Tile& t) const {
     const int b = tile / (mt * nt), l = tile - b * (mt * nt);
-    const int m = (l % mt) * bm, n = (l / mt) * kBN;
+    const int m = (l % mt) * SIDE, n = (l / mt) * SIDE;
     t.p[0] = b;
     t.p[1] = m;
     t.p[2] = n;
@@ -360,9 +385,63 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const
   }
 }
 
+// s A from its parts, added in order: a block takes 32 x 32 elements of one
+// matrix's upper tiles and writes them and, off the diagonal tiles, their mirror
+// image.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts, int nb, int pp,
+                                                        int side, float inv_s, __half* __restrict__ gram) {
+  __shared__ float tile[32][33];
+  ptx::let_next_grid_start();
+  ptx::wait_for_previous_grid();
+  const int nblk = pp / 32, r0 = (int)blockIdx.x / nblk * 32, c0 = (int)blockIdx.x % nblk * 32;
+  if (c0 / side < r0 / side) return;  // stored by its mirror image
+  const int b = (int)blockIdx.y, r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+  const int64_t one = (int64_t)pp * pp, at = b * one + (int64_t)(r0 + r) * pp + c0 + c;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part + (int64_t)p * nb * one + at));
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  s.x *= inv_s, s.y *= inv_s, s.z *= inv_s, s.w *= inv_s;
+  const __half2 lo = __floats2half2_rn(s.x, s.y), hi = __floats2half2_rn(s.z, s.w);
+  *reinterpret_cast<uint2*>(gram + at) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (c0 / side == r0 / side) return;
+  tile[r][c] = s.x, tile[r][c + 1] = s.y, tile[r][c + 2] = s.z, tile[r][c + 3] = s.w;
+  __syncthreads();
+  const __half2 tl = __floats2half2_rn(tile[c][r], tile[c + 1][r]), th = __floats2half2_rn(tile[c + 2][r], tile[c + 3][r]);
+  *reinterpret_cast<uint2*>(gram + b * one + (int64_t)(c0 + r) * pp + r0 + c) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&tl), *reinterpret_cast<const uint32_t*>(&th));
+}
+
+// Tiles are 256 x 256 of a pair of SMs, or 128 x 128 of one where those are at
+// most two for each SM in the largest product (a X + B X): then more SMs, an
+// epilogue of half the columns and no pair to set up shorten each launch
+// (measured: eight 512 x 128 96 us, 127 with pairs; 7168 x 256 141 and 178; four
+// 2048 x 512 178 and 200; two 2048 x 2048, 512 such tiles, 519 and 381).
+constexpr int kSms = 148;
+inline bool small_tiles(int64_t nb, int64_t mp, int64_t np) {
+  return nb * ceil_div(mp, 128) * ceil_div(np, 128) <= 2 * kSms;
+}
+inline int64_t square_tiles(int64_t pp, int64_t side) { return ceil_div(pp, side) * (ceil_div(pp, side) + 1) / 2; }
+
+// Parts that A's sum is cut into: as many as give every SM (pair) a tile, of at
+// least four k blocks each and no more than the parts' buffer (at most as large
+// as the stack in fp32) holds; none for sums below 16 k blocks, which the launch
+// that adds the parts would not pay for (measured: one 512 x 128 134 us in parts,
+// 129 without; 1024 x 128 133 and 139; 2048 x 256 158 and 182).
+inline int64_t units_of(int64_t pp, int64_t side) { return kSms / (side / 128) / square_tiles(pp, side); }
+inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
+  const int64_t nkb = std::max(mp, np) / BK;
+  if (nkb < 16) return 1;
+  const int64_t units = small_tiles(nb, mp, np) ? units_of(pp, 128) : units_of(pp, 256);
+  return std::max<int64_t>(1, std::min({units / nb, nkb / 4, mp * np / (pp * pp)}));
+}
+
 struct OrthPlan {
   int64_t mp, np, pp, chunks;
-  int64_t part, inv, x, xh0, xh1, gram, poly, total;  // byte offsets in the workspace
+  int64_t part, inv, x, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
 };
 
 inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
@@ -384,6 +463,9 @@ inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
   p.xh1 = take(nb * p.mp * p.np * 2);
   p.gram = take(nb * p.pp * p.pp * 2);
   p.poly = take(nb * p.pp * p.pp * 2);
+  // room for any batch's parts up to nb matrices
+  p.sums = take(std::min(std::max(units_of(p.pp, 128), units_of(p.pp, 256)), nb * (p.mp * p.np / (p.pp * p.pp))) *
+                p.pp * p.pp * 4);
   p.total = off;
   return p;
 }
@@ -394,8 +476,8 @@ int64_t orthogonalize_ws_bytes(int64_t nb, int64_t rows, int64_t cols) {
   return mm::orth_plan(nb, rows, cols).total;
 }
 
-// One batch of the stack that the workspace holds at once.
-static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols, bool g_f32, int steps,
+// One batch (nb matrices) of the stack (`stack` matrices), as the workspace holds it at once.
+static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int rows, int cols, bool g_f32, int steps,
                                        float a, float b, float c, float eps, float scale, void* out,
                                        char* ws, cudaStream_t s, const char** why) {
   using namespace mm;
@@ -445,10 +527,10 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
   if (e != cudaSuccess) return e;
 
   const bool left = rows <= cols;
-  constexpr int CG = 2;
   const CUtensorMapDataType f32t = CU_TENSOR_MAP_DATA_TYPE_FLOAT32, f16t = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap xk[2], xmn[2], gk, pk;       // operands: X K-major and MN-major, A and B K-major
   CUtensorMap g_in, x_io, xh_out[2], g_io, p_out, o_out = {};  // the epilogues' boxes
+  // MN rows of an operand in one CTA are 128 either way
   bool ok = make_operand(&gk, gram, false, nb * P.pp, P.pp, false, 128) &&
             make_operand(&pk, poly, false, nb * P.pp, P.pp, false, 128) &&
             make_boxes(&x_io, x32, f32t, 4, nb, P.mp, P.np, 128) && make_boxes(&g_io, gram, f16t, 2, nb, P.pp, P.pp, 64) &&
@@ -463,37 +545,54 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int rows, int cols
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  auto square = [&](auto op, const CUtensorMap& tm, int64_t k, int64_t k_rows) {
-    op.st = st;
-    op.k_rows = (int)k_rows;
-    op.nkb = (int)(k / BK);
-    op.bm = BM * CG;
-    const int64_t mt = ceil_div(P.pp, op.bm), nt = ceil_div(P.pp, op.kBN), r = op.kBN / op.bm;
-    op.tiles = (int)(r * nt * (nt + 1) / 2 - (r * nt - mt));  // the last column may lack its last tile
-    const Maps maps = {tm, tm, {op.kPoly ? p_out : g_io, g_io, g_io}};
-    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles, status, s, true);
-  };
-  auto apply = [&](auto op, const CUtensorMap& ta, const CUtensorMap& tb, int out_buf) {
-    op.st = st;
-    op.nkb = (int)(P.pp / BK);
-    op.bm = BM * CG;
-    op.mt = (int)ceil_div(P.mp, op.bm);
-    op.nt = (int)ceil_div(P.np, op.kBN);
-    const Maps maps = {ta, tb, {st.from_g ? g_in : x_io, x_io, st.last ? o_out : xh_out[out_buf]}};
-    return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s, true);
-  };
-  for (int i = 0; i < steps; ++i) {
-    const int in = i & 1;
-    st.from_g = i == 0 && g_state;
-    st.last = i == steps - 1;
-    e = left ? square(Square<false, false>{}, xk[in], P.np, P.mp) : square(Square<true, false>{}, xmn[in], P.mp, P.mp);
-    if (e != cudaSuccess) return e;
-    e = square(Square<false, true>{}, gk, P.pp, P.pp);
-    if (e != cudaSuccess) return e;
-    e = left ? apply(Apply<true>{}, pk, xmn[in], in ^ 1) : apply(Apply<false>{}, xk[in], pk, in ^ 1);
-    if (e != cudaSuccess) return e;
+  const int parts = (int)gram_parts(stack, P.mp, P.np, P.pp);  // of the whole stack: the passes do not change the bits
+  float* sums = reinterpret_cast<float*>(ws + P.sums);
+  CUtensorMap sums_out = {};
+  if (parts > 1 && !make_boxes(&sums_out, sums, f32t, 4, (int64_t)parts * nb, P.pp, P.pp, 128)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
   }
-  return cudaSuccess;
+  auto run = [&](auto side, auto leftc) {
+    constexpr int SIDE = decltype(side)::value, CG = SIDE / BM;
+    constexpr bool LEFT = decltype(leftc)::value, MN = !LEFT;
+    auto square = [&](auto op, const CUtensorMap& tm, int64_t k, int64_t k_rows, const CUtensorMap& result, int cuts) {
+      op.st = st;
+      op.k_rows = (int)k_rows;
+      op.nkb = (int)(k / BK);
+      op.parts = cuts;
+      op.tiles = (int)square_tiles(P.pp, SIDE);
+      const Maps maps = {tm, tm, {result, g_io, g_io}};
+      return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles * cuts, status, s, true);
+    };
+    for (int i = 0; i < steps; ++i) {
+      const int in = i & 1;
+      const CUtensorMap& x = LEFT ? xk[in] : xmn[in];
+      const int64_t k = LEFT ? P.np : P.mp;
+      st.from_g = i == 0 && g_state;
+      st.last = i == steps - 1;
+      cudaError_t e = parts == 1 ? square(Square<MN, kGram, SIDE>{}, x, k, P.mp, g_io, 1)
+                                 : square(Square<MN, kPart, SIDE>{}, x, k, P.mp, sums_out, parts);
+      if (e == cudaSuccess && parts > 1)
+        e = launch_overlapped(sum_parts_kernel, dim3((unsigned)((P.pp / 32) * (P.pp / 32)), (unsigned)nb), 256, s,
+                              (const float*)sums, parts, nb, (int)P.pp, SIDE, st.inv_s, reinterpret_cast<__half*>(gram));
+      if (e == cudaSuccess) e = square(Square<false, kPoly, SIDE>{}, gk, P.pp, P.pp, p_out, 1);
+      if (e != cudaSuccess) return e;
+      Apply<LEFT, SIDE> op;
+      op.st = st;
+      op.nkb = (int)(P.pp / BK);
+      op.mt = (int)ceil_div(P.mp, SIDE);
+      op.nt = (int)ceil_div(P.np, SIDE);
+      const Maps maps = {LEFT ? pk : xk[in], LEFT ? xmn[in] : pk,
+                         {st.from_g ? g_in : x_io, x_io, st.last ? o_out : xh_out[in ^ 1]}};
+      e = launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s, true);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  };
+  using Small = std::integral_constant<int, 128>;
+  using Pair = std::integral_constant<int, 256>;
+  if (small_tiles(stack, P.mp, P.np)) return left ? run(Small{}, std::true_type{}) : run(Small{}, std::false_type{});
+  return left ? run(Pair{}, std::true_type{}) : run(Pair{}, std::false_type{});
 }
 
 cudaError_t launch_orthogonalize(const void* g, int nb, int rows, int cols, bool g_f32, int steps, float a,
@@ -507,7 +606,7 @@ cudaError_t launch_orthogonalize(const void* g, int nb, int rows, int cols, bool
   const size_t in_bytes = (size_t)rows * cols * (g_f32 ? 4 : 2), out_bytes = (size_t)rows * cols * 2;
   for (int64_t i = 0; i < nb; i += at_once) {
     const int n = (int)std::min<int64_t>(at_once, nb - i);
-    cudaError_t e = orthogonalize_batch(static_cast<const char*>(g) + i * in_bytes, n, rows, cols, g_f32, steps, a, b,
+    cudaError_t e = orthogonalize_batch(static_cast<const char*>(g) + i * in_bytes, n, nb, rows, cols, g_f32, steps, a, b,
                                         c, eps, scale, static_cast<char*>(out) + i * out_bytes,
                                         static_cast<char*>(ws), s, why);
     if (e != cudaSuccess) return e;

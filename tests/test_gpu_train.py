@@ -432,7 +432,7 @@ def test_orthogonalize_zero_and_nan_matrices_stay_apart():
     assert torch.isnan(out[3]).all() and torch.isnan(out[4]).all()
 
 
-@pytest.mark.parametrize("shape", [(7, 72, 136), (7, 137, 61)])
+@pytest.mark.parametrize("shape", [(7, 72, 136), (7, 137, 61), (7, 72, 2500), (7, 3100, 260)])
 def test_orthogonalize_in_passes_equals_at_once(shape):
     """A workspace that holds some of the stack: the same bits."""
     G = _randn(_gen(8), *shape, dtype=torch.float32)
