@@ -89,7 +89,8 @@ cudaError_t noalloc_status(int32_t* out, bool clear);
 // training (gemm_grad.cu, combine_grad.cu, orthogonalize.cu)
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int32_t* status, cudaStream_t s, const char** why);
+                                 int max_rows_per_expert, int32_t* status, cudaStream_t s,
+                                 const char** why);
 cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
                                  int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
                                  cudaStream_t s, const char** why);
@@ -525,7 +526,8 @@ moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t
   if (overlaps(dA, out, h, M * K * 2)) return fail(MOE_ERR_INVALID_ARG, "dA and h overlap");
   MOE_TRY(check_device());
   const char* why = "";
-  cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h, at<int32_t>(ws, 0),
+  cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h, max_rows_per_expert,
+                                       at<int32_t>(ws, 0),
                                        static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM row gradient: %s %s", cudaGetErrorString(e), why);
   return ok();

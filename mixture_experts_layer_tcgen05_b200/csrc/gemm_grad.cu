@@ -51,38 +51,60 @@ __device__ __forceinline__ void load_row32(const __nv_bfloat16* src, float (&v)[
   }
 }
 
-// Tiles of 128 rows of one expert by 256 columns, in the order of the forward's
-// 128-row GEMM: expert, band of m-tiles, n-tile, m-tile.
+// Tiles of one expert's rows by 256 columns, in the order of the forward's
+// 128-row GEMM: expert, band of m-tiles, n-tile, m-tile. PAIR: 256 rows of a
+// pair of SMs, else 128. A k block of a 128-row tile brings 48 KB for 512 cycles
+// of MMA (the pair's 32 KB per SM), which at full rate is more than L2 delivers;
+// but an expert's last 128 rows or fewer would leave half a pair's tile empty.
+// So an expert's rows go to pairs as far as they fill more than half a tile, and
+// a remainder of at most 128 rows to single SMs, in a second launch that starts
+// as the first one's SMs run out of tiles.
 // ACT: the product is the gradient d of h = a(g) u; the epilogue writes
 // dg = d u a'(g), du = d a(g) and, with h given, a(g) u.
-template <int ACT>
+enum RowSet { kAllRows, kPairRows, kRestRows };
+
+template <int ACT, bool PAIR>
 struct RowGrad {
   static constexpr bool kAMn = false, kBMn = true, kTail = false;
   static constexpr int kBN = 256, kFmt = 1, kChunk = 0;
-  static constexpr int kStageWarp = 0, kSharedInts = 2 * (gg::kMaxE + 1);
+  // A pair stages boxes of 32 x 32: the result; gated, two of g and u each, which
+  // their gradients replace, and one of h. A single SM's wider stages leave no
+  // room for that beside enough of them, and its rows rarely fill a box.
+  static constexpr int kStageWarp = !PAIR ? 0 : ACT == kActNone ? 2048 : 10 * 1024;
+  static constexpr int kSharedInts = 2 * (gg::kMaxE + 1);
+  static constexpr int kRows = PAIR ? 2 * BM : BM;
 
   const int32_t* offsets;
   int E, M_total, N, K, NT, band;
+  RowSet set;
   const __nv_bfloat16* gu;  // [M_total, 2K]
   __nv_bfloat16* dA;        // [M_total, K], with ACT [M_total, 2K]
   __nv_bfloat16* h;         // [M_total, K] or nullptr
 
+  // m-tiles of an expert with c rows, and its first row in them
+  __device__ __forceinline__ int m_tiles(int c) const {
+    if (PAIR) return c / 256 + (c % 256 > 128);
+    if (set == kRestRows) return c % 256 >= 1 && c % 256 <= 128;
+    return (c + BM - 1) / BM;
+  }
+  __device__ __forceinline__ int first_row(int c) const { return !PAIR && set == kRestRows ? c / 256 * 256 : 0; }
+
   __device__ void setup(int32_t* sh) const {
-    load_offsets(offsets, E, M_total, sh + gg::kMaxE + 1);
-    ragged_tile_starts(sh + gg::kMaxE + 1, E, BM, NT, sh);
+    int32_t* soff = sh + gg::kMaxE + 1;
+    load_offsets(offsets, E, M_total, soff);
+    tile_starts(E, sh, [&](int e) { return m_tiles(max(soff[e + 1] - soff[e], 0)) * NT; });
   }
   __device__ int total(const int32_t* sh) const { return sh[E]; }
   __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
     const int32_t* soff = sh + gg::kMaxE + 1;
     const int e = gg::find_expert(sh, E, tile);
-    const int local = tile - sh[e];
-    const int mt = (soff[e + 1] - soff[e] + BM - 1) / BM;
+    const int local = tile - sh[e], c = soff[e + 1] - soff[e];
     const int bsz = band * NT;
     const int b = local / bsz;
-    const int rows = min(band, mt - b * band);
+    const int rows = min(band, m_tiles(c) - b * band);
     const int l2 = local - b * bsz;
     const int n = l2 / rows, m = b * band + l2 % rows;
-    t.a_mn = soff[e] + m * BM;
+    t.a_mn = soff[e] + first_row(c) + m * kRows;
     t.a_k = 0;
     t.b_mn = n * kBN;
     t.b_k = e * N;
@@ -90,35 +112,106 @@ struct RowGrad {
     t.tail = BK;
     t.p[0] = soff[e + 1];
   }
-  __device__ void prefetch(const Tile&, Warp&) const {}
+  __device__ __forceinline__ int steps(const Tile& t, const Warp& w) const {
+    if (w.row0(t.a_mn) >= t.p[0]) return 0;
+    return max(0, min(kBN / 2, K - t.b_mn - w.half * (kBN / 2))) / 32;
+  }
+  __device__ __forceinline__ void load_gu(const Tile& t, Warp& w, int i) const {
+    const int col = t.b_mn + w.half * (kBN / 2) + 32 * i, row0 = w.row0(t.a_mn);
+    const uint32_t box = w.base + (i & 1) * 4096;
+    if (w.lane == 0) {
+      ptx::mbar_arrive_expect_tx(w.bar + 8 * (i & 1), 4096);
+      ptx::tma_load_3d(box, &w.maps->c[1], col, row0, 0, w.bar + 8 * (i & 1));
+      ptx::tma_load_3d(box + 2048, &w.maps->c[1], K + col, row0, 0, w.bar + 8 * (i & 1));
+    }
+    w.pending |= 1u << (i & 1);
+  }
+  __device__ void prefetch(const Tile& t, Warp& w) const {
+    if constexpr (PAIR && ACT != kActNone) {
+      if (steps(t, w) == 0) return;
+      w.free_boxes();
+      load_gu(t, w, 0);
+    }
+  }
+  static __device__ __forceinline__ void put_row(uint32_t box, int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      Warp::put(Warp::at64(box, lane, u),
+                make_uint4(pack_bf16x2(v[8 * u], v[8 * u + 1]), pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                           pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), pack_bf16x2(v[8 * u + 6], v[8 * u + 7])));
+  }
+  static __device__ __forceinline__ void get_row(uint32_t box, int lane, float (&v)[32]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint4 x = Warp::get(Warp::at64(box, lane, u));
+      v[8 * u] = bf16lo_to_f32(x.x), v[8 * u + 1] = bf16hi_to_f32(x.x);
+      v[8 * u + 2] = bf16lo_to_f32(x.y), v[8 * u + 3] = bf16hi_to_f32(x.y);
+      v[8 * u + 4] = bf16lo_to_f32(x.z), v[8 * u + 5] = bf16hi_to_f32(x.z);
+      v[8 * u + 6] = bf16lo_to_f32(x.w), v[8 * u + 7] = bf16hi_to_f32(x.w);
+    }
+  }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
-    const int row = w.row0(t.a_mn) + w.lane, half = w.half;
+    const int row0 = w.row0(t.a_mn), row = row0 + w.lane, n = steps(t, w);
     const bool valid = row < t.p[0];
+    // a box reaches past the expert's rows: what is past them is not this
+    // expert's to write, so each lane stores its own row
+    const bool boxed = PAIR && row0 + 32 <= t.p[0];
 #pragma unroll 1
-    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2) && t.b_mn + c < K; c += 32) {
+    for (int i = 0; i < n; ++i) {
+      const int c = w.half * (kBN / 2) + 32 * i, col = t.b_mn + c;
+      const uint32_t box = w.base + (i & 1) * 4096;
+      if constexpr (PAIR) {
+        w.free_boxes();
+        if (ACT != kActNone && i + 1 < n) load_gu(t, w, i + 1);
+      }
       float d[32];
       load_acc32(taddr + c, false, d);
-      if (!valid) continue;
-      const int col = t.b_mn + c;
       if constexpr (ACT == kActNone) {
-        gg::store_row32(dA + (int64_t)row * K + col, d);
-      } else {
-        const __nv_bfloat16* gsrc = gu + (int64_t)row * 2 * K + col;
-        __nv_bfloat16* out = dA + (int64_t)row * 2 * K + col;
-        float g[32], u[32];
-        load_row32(gsrc, g);
-        load_row32(gsrc + K, u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a, da;
-          act_grad<ACT>(g[i], a, da);
-          g[i] = d[i] * u[i] * da;
-          d[i] *= a;
-          u[i] *= a;
+        if (boxed) {
+          put_row(w.base, w.lane, d);
+          w.publish();
+          if (w.lane == 0) {
+            ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, 0);
+            ptx::bulk_commit();
+          }
+        } else if (valid) {
+          gg::store_row32(dA + (int64_t)row * K + col, d);
         }
-        gg::store_row32(out, g);
-        gg::store_row32(out + K, d);
-        if (h) gg::store_row32(h + (int64_t)row * K + col, u);
+      } else {
+        const int64_t at = (int64_t)row * 2 * K + col;
+        float g[32], u[32];
+        if constexpr (PAIR) {
+          if (!w.wait(i & 1)) return false;
+          get_row(box, w.lane, g);
+          get_row(box + 2048, w.lane, u);
+        } else if (valid) {
+          load_row32(gu + at, g);
+          load_row32(gu + at + K, u);
+        }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          float a, da;
+          act_grad<ACT>(g[q], a, da);
+          g[q] = d[q] * u[q] * da;
+          d[q] *= a;
+          u[q] *= a;
+        }
+        if (boxed) {
+          put_row(box, w.lane, g);
+          put_row(box + 2048, w.lane, d);
+          if (h) put_row(w.base + 8192, w.lane, u);
+          w.publish();
+          if (w.lane == 0) {
+            ptx::tma_store_3d(&w.maps->c[0], box, col, row0, 0);
+            ptx::tma_store_3d(&w.maps->c[0], box + 2048, K + col, row0, 0);
+            if (h) ptx::tma_store_3d(&w.maps->c[2], w.base + 8192, col, row0, 0);
+            ptx::bulk_commit();
+          }
+        } else if (valid) {
+          gg::store_row32(dA + at, g);
+          gg::store_row32(dA + at + K, d);
+          if (h) gg::store_row32(h + (int64_t)row * K + col, u);
+        }
       }
     }
     return true;
@@ -185,32 +278,52 @@ struct WeightGrad {
 
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int32_t* status, cudaStream_t s, const char** why) {
-  mm::Maps maps = {};
-  if (!mm::make_operand(&maps.a, dC, true, M_total, N, false, mm::BM) ||
-      !mm::make_operand(&maps.b, B, true, (int64_t)E * N, K, true, 256)) {
+                                 int max_rows_per_expert, int32_t* status, cudaStream_t s, const char** why) {
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int64_t out_cols = act == kActNone ? K : 2 * (int64_t)K;
+  mm::Maps pair = {}, single = {};
+  if (!mm::make_operand(&single.a, dC, true, M_total, N, false, mm::BM) ||
+      !mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256) ||
+      !mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128) ||
+      !mm::make_boxes(&pair.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) ||
+      (gu && !mm::make_boxes(&pair.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) ||
+      (h && !mm::make_boxes(&pair.c[2], h, bf16, 2, 1, M_total, K, 64))) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  auto go = [&](auto op) {
+  pair.a = single.a;
+  // no expert fills more than half a pair's tile: one launch over all rows
+  const int most = max_rows_per_expert > 0 ? std::min(max_rows_per_expert, M_total) : M_total;
+  const bool pairs = most > mm::BM;
+  auto go = [&](auto op, auto cg, mm::RowSet set, bool overlap) {
+    constexpr int CG = decltype(cg)::value;
     op.offsets = offsets;
     op.E = E;
     op.M_total = M_total;
     op.N = N;
     op.K = K;
     op.NT = (int)ceil_div(K, op.kBN);
-    op.band = 16;
+    op.band = 16 / CG;
+    op.set = set;
     op.gu = static_cast<const __nv_bfloat16*>(gu);
     op.dA = static_cast<__nv_bfloat16*>(dA);
     op.h = static_cast<__nv_bfloat16*>(h);
-    const int64_t tiles = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * op.NT;
-    return mm::launch<decltype(op), 1>(maps, op, tiles, status, s);
+    const int64_t tiles = ((int64_t)M_total / op.kRows + std::min(M_total, E)) * op.NT;
+    return mm::launch<decltype(op), CG>(CG == 2 ? pair : single, op, tiles, status, s, overlap);
+  };
+  auto both = [&](auto act_c) {
+    constexpr int ACT = decltype(act_c)::value;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (!pairs) return go(mm::RowGrad<ACT, false>{}, One{}, mm::kAllRows, false);
+    cudaError_t e = go(mm::RowGrad<ACT, true>{}, Two{}, mm::kPairRows, false);
+    return e != cudaSuccess ? e : go(mm::RowGrad<ACT, false>{}, One{}, mm::kRestRows, false);
   };
   switch (act) {
-    case kActSilu: return go(mm::RowGrad<kActSilu>{});
-    case kActGelu: return go(mm::RowGrad<kActGelu>{});
-    case kActRelu: return go(mm::RowGrad<kActRelu>{});
-    default: return go(mm::RowGrad<kActNone>{});
+    case kActSilu: return both(std::integral_constant<int, kActSilu>{});
+    case kActGelu: return both(std::integral_constant<int, kActGelu>{});
+    case kActRelu: return both(std::integral_constant<int, kActRelu>{});
+    default: return both(std::integral_constant<int, kActNone>{});
   }
 }
 

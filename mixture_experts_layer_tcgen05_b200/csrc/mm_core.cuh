@@ -504,16 +504,15 @@ __device__ __forceinline__ void load_offsets(const int32_t* offsets, int E, int 
   __syncwarp();
 }
 
-// tile_start[e] = number of tiles of the experts before e, each having
-// ceil(rows / rows_per_tile) * per_row_tile; tile_start[E] = their total. Warp-wide.
-__device__ __forceinline__ void ragged_tile_starts(const int32_t* soff, int E, int rows_per_tile,
-                                                   int per_row_tile, int32_t* tile_start) {
+// tile_start[e] = number of tiles of the experts before e, tiles(e) each;
+// tile_start[E] = their total. Warp-wide.
+template <class F>
+__device__ __forceinline__ void tile_starts(int E, int32_t* tile_start, F tiles) {
   const int lane = threadIdx.x & 31;
   int32_t carry = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    const int rows = e < E ? max(soff[e + 1] - soff[e], 0) : 0;
-    const int32_t t = (rows + rows_per_tile - 1) / rows_per_tile * per_row_tile;
+    const int32_t t = e < E ? tiles(e) : 0;
     int32_t incl = t;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
