@@ -165,8 +165,8 @@ def _s(stream):
 def _nbytes(ws, ws_bytes):
     if ws_bytes is not None:
         return ws_bytes
-    if hasattr(ws, "numel"):
-        return ws.numel() * ws.element_size()
+    if hasattr(ws, "nbytes"):
+        return ws.nbytes
     raise ValueError("ws_bytes is required for a raw workspace address")
 
 

@@ -89,11 +89,11 @@ cudaError_t noalloc_status(int32_t* out, bool clear);
 // training (gemm_grad.cu, combine_grad.cu, orthogonalize.cu)
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int max_rows_per_expert, int32_t* status, cudaStream_t s,
-                                 const char** why);
+                                 int max_rows_per_expert, int32_t* status, void* scratch,
+                                 size_t scratch_bytes, cudaStream_t s, const char** why);
 cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
                                  int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
-                                 cudaStream_t s, const char** why);
+                                 void* scratch, size_t scratch_bytes, cudaStream_t s, const char** why);
 cudaError_t launch_combine_backward(const void* dout, const void* y, const float* w, const int32_t* inv,
                                     int T, int H, int k, void* dy, float* dw, int32_t* status,
                                     cudaStream_t s);
@@ -519,15 +519,20 @@ moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t
   if (ws_bytes < 256) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes", ws_bytes);
   const uint64_t M = (uint64_t)M_total, out = M * K * 2 * (ep == MOE_EPILOGUE_NONE ? 1 : 2);
   const struct { const void* p; uint64_t n; const char* name; } in[] = {
-      {dC, M * N * 2, "dC"}, {B, (uint64_t)E * N * K * 2, "B"}, {gu, M * K * 4, "gu"}, {ws, ws_bytes, "ws"}};
-  for (const auto& i : in)
+      {dC, M * N * 2, "dC"}, {B, (uint64_t)E * N * K * 2, "B"}, {gu, M * K * 4, "gu"},
+      {offsets, (uint64_t)(E + 1) * 4, "expert_offsets"}, {ws, 256, "ws"}};
+  bool scratch = true;  // buffers that live in the workspace themselves leave no room for partial sums in it
+  for (const auto& i : in) {
     if (overlaps(dA, out, i.p, i.n) || overlaps(h, M * K * 2, i.p, i.n))
       return fail(MOE_ERR_INVALID_ARG, "an output overlaps %s", i.name);
+    scratch &= i.p == ws || !overlaps(ws, ws_bytes, i.p, i.n);
+  }
+  scratch &= !overlaps(ws, ws_bytes, dA, out) && !overlaps(ws, ws_bytes, h, M * K * 2);
   if (overlaps(dA, out, h, M * K * 2)) return fail(MOE_ERR_INVALID_ARG, "dA and h overlap");
   MOE_TRY(check_device());
   const char* why = "";
   cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h, max_rows_per_expert,
-                                       at<int32_t>(ws, 0),
+                                       at<int32_t>(ws, 0), at<char>(ws, 256), scratch ? ws_bytes - 256 : 0,
                                        static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM row gradient: %s %s", cudaGetErrorString(e), why);
   return ok();
@@ -547,12 +552,21 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dC, const void* A, const int32_t
   MOE_TRY(check_ptr(ws, "ws"));
   if (ws_bytes < 256) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes", ws_bytes);
   const uint64_t M = (uint64_t)M_total, out = (uint64_t)E * N * K * (type == MOE_GRAD_F32 ? 4 : 2);
-  if (overlaps(dB, out, dC, M * N * 2) || overlaps(dB, out, A, M * K * 2) || overlaps(dB, out, ws, ws_bytes))
+  const struct { const void* p; uint64_t n; } in[] = {
+      {dC, M * N * 2}, {A, M * K * 2}, {offsets, (uint64_t)(E + 1) * 4}, {ws, 256}};
+  bool scratch = !overlaps(ws, ws_bytes, dB, out);  // as in moe_grouped_gemm_dgrad
+  bool clash = false;
+  for (const auto& i : in) {
+    clash |= overlaps(dB, out, i.p, i.n);
+    scratch &= i.p == ws || !overlaps(ws, ws_bytes, i.p, i.n);
+  }
+  if (clash)
     return fail(MOE_ERR_INVALID_ARG, "dB overlaps an input or the workspace");
   MOE_TRY(check_device());
   const char* why = "";
   cudaError_t e = launch_grouped_wgrad(dC, A, offsets, M_total, E, N, K, type == MOE_GRAD_F32, accumulate != 0, dB,
-                                       at<int32_t>(ws, 0), static_cast<cudaStream_t>(stream), &why);
+                                       at<int32_t>(ws, 0), at<char>(ws, 256), scratch ? ws_bytes - 256 : 0,
+                                       static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM weight gradient: %s %s", cudaGetErrorString(e), why);
   return ok();
 }

@@ -77,6 +77,8 @@ struct RowGrad {
   const int32_t* offsets;
   int E, M_total, N, K, NT, band;
   RowSet set;
+  int parts;    // ranges of n that run as tiles of their own; above 1, single SMs only, and
+  float* part;  // their fp32 sums go here, [parts, M_total, K]
   const __nv_bfloat16* gu;  // [M_total, 2K]
   __nv_bfloat16* dA;        // [M_total, K], with ACT [M_total, 2K]
   __nv_bfloat16* h;         // [M_total, K] or nullptr
@@ -94,9 +96,19 @@ struct RowGrad {
     load_offsets(offsets, E, M_total, soff);
     tile_starts(E, sh, [&](int e) { return m_tiles(max(soff[e + 1] - soff[e], 0)) * NT; });
   }
-  __device__ int total(const int32_t* sh) const { return sh[E]; }
+  static constexpr bool kParts = !PAIR && ACT == kActNone;
+  __device__ int total(const int32_t* sh) const { return sh[E] * (kParts ? parts : 1); }
   __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
     const int32_t* soff = sh + gg::kMaxE + 1;
+    t.nkb = N / BK;
+    int kb0 = 0;
+    if constexpr (kParts) {
+      const int p = tile % parts, nkb = t.nkb;
+      tile /= parts;
+      kb0 = (int)((int64_t)nkb * p / parts);
+      t.nkb = (int)((int64_t)nkb * (p + 1) / parts) - kb0;
+      t.p[1] = p;
+    }
     const int e = gg::find_expert(sh, E, tile);
     const int local = tile - sh[e], c = soff[e + 1] - soff[e];
     const int bsz = band * NT;
@@ -105,10 +117,9 @@ struct RowGrad {
     const int l2 = local - b * bsz;
     const int n = l2 / rows, m = b * band + l2 % rows;
     t.a_mn = soff[e] + first_row(c) + m * kRows;
-    t.a_k = 0;
+    t.a_k = kb0 * BK;
     t.b_mn = n * kBN;
-    t.b_k = e * N;
-    t.nkb = N / BK;
+    t.b_k = e * N + kb0 * BK;
     t.tail = BK;
     t.p[0] = soff[e + 1];
   }
@@ -174,6 +185,12 @@ struct RowGrad {
             ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, 0);
             ptx::bulk_commit();
           }
+        } else if (kParts && part) {
+          if (valid) {
+            float4* dst = reinterpret_cast<float4*>(part + ((int64_t)t.p[1] * M_total + row) * K + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+          }
         } else if (valid) {
           gg::store_row32(dA + (int64_t)row * K + col, d);
         }
@@ -218,6 +235,60 @@ struct RowGrad {
   }
 };
 
+// The row gradient from its parts, added in order: a warp per row, 256 columns a
+// block step. Rows of no expert are left alone.
+template <int ACT>
+__global__ void __launch_bounds__(256)
+    sum_rows_kernel(const float* __restrict__ part, int parts, const int32_t* __restrict__ offsets, int E, int M_total,
+                    int K, const __nv_bfloat16* __restrict__ gu, __nv_bfloat16* __restrict__ dA,
+                    __nv_bfloat16* __restrict__ h) {
+  ptx::wait_for_previous_grid();
+  const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= M_total) return;
+  bool mine = false;
+  for (int e = lane; e < E; e += 32) mine |= __ldg(offsets + e) <= row && row < __ldg(offsets + e + 1);
+  if (!__any_sync(0xffffffffu, mine)) return;
+  const int64_t slice = (int64_t)M_total * K;
+  for (int col = ((int)blockIdx.y * 32 + lane) * 8; col < K; col += (int)gridDim.y * 256) {
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = 0.0f;
+    const float* src = part + (int64_t)row * K + col;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float4 lo = __ldg(reinterpret_cast<const float4*>(src + p * slice));
+      const float4 hi = __ldg(reinterpret_cast<const float4*>(src + p * slice) + 1);
+      d[0] += lo.x, d[1] += lo.y, d[2] += lo.z, d[3] += lo.w;
+      d[4] += hi.x, d[5] += hi.y, d[6] += hi.z, d[7] += hi.w;
+    }
+    auto store = [](__nv_bfloat16* dst, const float (&v)[8]) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    };
+    if constexpr (ACT == kActNone) {
+      store(dA + (int64_t)row * K + col, d);
+    } else {
+      const int64_t at = (int64_t)row * 2 * K + col;
+      const uint4 gv = __ldg(reinterpret_cast<const uint4*>(gu + at)), uv = __ldg(reinterpret_cast<const uint4*>(gu + at + K));
+      const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
+      float dg[8], hv[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = i & 1 ? bf16hi_to_f32(gw[i / 2]) : bf16lo_to_f32(gw[i / 2]);
+        const float u = i & 1 ? bf16hi_to_f32(uw[i / 2]) : bf16lo_to_f32(uw[i / 2]);
+        float a, da;
+        act_grad<ACT>(g, a, da);
+        dg[i] = d[i] * u * da;
+        d[i] *= a;
+        hv[i] = a * u;
+      }
+      store(dA + at, dg);
+      store(dA + at + K, d);
+      if (h) store(h + (int64_t)row * K + col, hv);
+    }
+  }
+}
+
 // ----------------------------------------------------------- weight gradient
 // Tiles of 128 CG by 256 of one expert's [N, K] gradient, summed over its rows.
 // Experts without rows get zeros (or are left as they are when adding).
@@ -229,12 +300,19 @@ struct WeightGrad {
 
   const int32_t* offsets;
   int E, M_total, N, K, mt, nt, bm;
+  int parts;  // ranges of rows that run as tiles of their own; above 1, their fp32 sums are items part * E + e
 
   __device__ void setup(int32_t* sh) const {
     load_offsets(offsets, E, M_total, sh);
   }
-  __device__ int total(const int32_t*) const { return E * mt * nt; }
+  static constexpr bool kParts = F32 && !ADD;
+  __device__ int total(const int32_t*) const { return E * mt * nt * (kParts ? parts : 1); }
   __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
+    int p = 0;
+    if constexpr (kParts) {
+      p = tile % parts;
+      tile /= parts;
+    }
     const int e = tile / (mt * nt), l = tile - e * (mt * nt);
     const int lo = sh[e], rows = max(sh[e + 1] - lo, 0);
     t.a_mn = (l % mt) * bm;
@@ -243,6 +321,13 @@ struct WeightGrad {
     t.nkb = (rows + BK - 1) / BK;
     t.tail = rows - (t.nkb - 1) * BK;
     t.p[0] = e;
+    if (kParts && parts > 1) {
+      const int kb0 = (int)((int64_t)t.nkb * p / parts), kb1 = (int)((int64_t)t.nkb * (p + 1) / parts);
+      if (kb1 < t.nkb) t.tail = BK;
+      t.a_k = t.b_k = lo + kb0 * BK;
+      t.nkb = kb1 - kb0;
+      t.p[0] = p * E + e;
+    }
   }
   __device__ void store(const Tile& t, Warp& w, const uint32_t (&d)[kBN / 2]) const {
     const int n = w.row0(t.a_mn), col = t.b_mn + w.half * (kBN / 2);
@@ -274,28 +359,71 @@ struct WeightGrad {
   }
 };
 
+// The weight gradient from its parts, added in order (and to dB's values).
+template <bool F32, bool ADD>
+__global__ void __launch_bounds__(256) sum_weights_kernel(const float4* __restrict__ part, int parts, int64_t n4,
+                                                          void* __restrict__ dB) {
+  ptx::wait_for_previous_grid();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float4 v = __ldg(part + p * n4 + i);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  if constexpr (F32) {
+    float4* dst = static_cast<float4*>(dB) + i;
+    if constexpr (ADD) {
+      const float4 o = *dst;
+      s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+    }
+    *dst = s;
+  } else {
+    static_cast<uint2*>(dB)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
+
+// Parts that a long sum of nkb k blocks is cut into where its tiles are fewer
+// than the SMs (pairs): as many as there are SMs for, of at least 8 k blocks,
+// and no more than the scratch holds; none below 32 k blocks, which the launch
+// that adds them would not pay for (measured: 4 experts' 100 rows, gated, K =
+// 512: N = 7168 in parts 26 us, without 49; N = 2048 25 and 25; one expert's
+// 16384 rows to 512 x 1024 30 and 87).
+inline int sum_parts(int64_t units, int64_t tiles, int64_t nkb, int64_t part_bytes, size_t scratch_bytes) {
+  if (nkb < 32) return 1;
+  const int64_t p = std::min({units / std::max<int64_t>(tiles, 1), nkb / 8, (int64_t)scratch_bytes / part_bytes});
+  return (int)std::max<int64_t>(1, p);
+}
+
 }  // namespace mm
 
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int max_rows_per_expert, int32_t* status, cudaStream_t s, const char** why) {
+                                 int max_rows_per_expert, int32_t* status, void* scratch, size_t scratch_bytes,
+                                 cudaStream_t s, const char** why) {
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int64_t out_cols = act == kActNone ? K : 2 * (int64_t)K;
+  // no expert fills more than half a pair's tile: one launch over all rows
+  const int most = max_rows_per_expert > 0 ? std::min(max_rows_per_expert, M_total) : M_total;
+  const int64_t tiles_ub = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * ceil_div(K, 256);
+  const int parts = mm::sum_parts(num_sms(), tiles_ub, N / mm::BK, (int64_t)M_total * K * 4, scratch_bytes);
+  const bool pairs = most > mm::BM && parts == 1;
   mm::Maps pair = {}, single = {};
-  if (!mm::make_operand(&single.a, dC, true, M_total, N, false, mm::BM) ||
-      !mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256) ||
-      !mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128) ||
-      !mm::make_boxes(&pair.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) ||
-      (gu && !mm::make_boxes(&pair.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) ||
-      (h && !mm::make_boxes(&pair.c[2], h, bf16, 2, 1, M_total, K, 64))) {
+  bool ok = mm::make_operand(&single.a, dC, true, M_total, N, false, mm::BM) &&
+            mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256);
+  if (pairs) {
+    pair.a = single.a;
+    ok = ok && mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128) &&
+         mm::make_boxes(&pair.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) &&
+         (!gu || mm::make_boxes(&pair.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) &&
+         (!h || mm::make_boxes(&pair.c[2], h, bf16, 2, 1, M_total, K, 64));
+  }
+  if (!ok) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  pair.a = single.a;
-  // no expert fills more than half a pair's tile: one launch over all rows
-  const int most = max_rows_per_expert > 0 ? std::min(max_rows_per_expert, M_total) : M_total;
-  const bool pairs = most > mm::BM;
-  auto go = [&](auto op, auto cg, mm::RowSet set, bool overlap) {
+  auto go = [&](auto op, auto cg, mm::RowSet set) {
     constexpr int CG = decltype(cg)::value;
     op.offsets = offsets;
     op.E = E;
@@ -305,19 +433,29 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
     op.NT = (int)ceil_div(K, op.kBN);
     op.band = 16 / CG;
     op.set = set;
+    op.parts = parts;
+    op.part = parts > 1 ? static_cast<float*>(scratch) : nullptr;
     op.gu = static_cast<const __nv_bfloat16*>(gu);
     op.dA = static_cast<__nv_bfloat16*>(dA);
     op.h = static_cast<__nv_bfloat16*>(h);
-    const int64_t tiles = ((int64_t)M_total / op.kRows + std::min(M_total, E)) * op.NT;
-    return mm::launch<decltype(op), CG>(CG == 2 ? pair : single, op, tiles, status, s, overlap);
+    const int64_t tiles = ((int64_t)M_total / op.kRows + std::min(M_total, E)) * op.NT * parts;
+    return mm::launch<decltype(op), CG>(CG == 2 ? pair : single, op, tiles, status, s);
   };
   auto both = [&](auto act_c) {
     constexpr int ACT = decltype(act_c)::value;
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
-    if (!pairs) return go(mm::RowGrad<ACT, false>{}, One{}, mm::kAllRows, false);
-    cudaError_t e = go(mm::RowGrad<ACT, true>{}, Two{}, mm::kPairRows, false);
-    return e != cudaSuccess ? e : go(mm::RowGrad<ACT, false>{}, One{}, mm::kRestRows, false);
+    if (parts > 1) {
+      cudaError_t e = go(mm::RowGrad<kActNone, false>{}, One{}, mm::kAllRows);
+      if (e != cudaSuccess) return e;
+      const dim3 grid((unsigned)ceil_div(M_total, 8), (unsigned)ceil_div(K, 1024));
+      return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, static_cast<const float*>(scratch), parts,
+                                   offsets, E, M_total, K, static_cast<const __nv_bfloat16*>(gu),
+                                   static_cast<__nv_bfloat16*>(dA), static_cast<__nv_bfloat16*>(h));
+    }
+    if (!pairs) return go(mm::RowGrad<ACT, false>{}, One{}, mm::kAllRows);
+    cudaError_t e = go(mm::RowGrad<ACT, true>{}, Two{}, mm::kPairRows);
+    return e != cudaSuccess ? e : go(mm::RowGrad<ACT, false>{}, One{}, mm::kRestRows);
   };
   switch (act) {
     case kActSilu: return both(std::integral_constant<int, kActSilu>{});
@@ -329,14 +467,19 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
 
 cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
                                  int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
-                                 cudaStream_t s, const char** why) {
+                                 void* scratch, size_t scratch_bytes, cudaStream_t s, const char** why) {
   mm::Maps maps = {};
   // A pair's tile is 256 rows of dB: with N = 128 half of it would be empty.
   const int pair = N > 128 ? 2 : 1;
+  const int64_t tiles = (int64_t)E * ceil_div(N, mm::BM * pair) * ceil_div(K, 256), n = (int64_t)E * N * K;
+  // (the rows an expert has are known on the device only: as if they were spread evenly)
+  const int parts = mm::sum_parts(num_sms() / pair, tiles, M_total / mm::BK / E, n * 4, scratch_bytes);
+  const bool wide = f32 || parts > 1;
   if (!mm::make_operand(&maps.a, dC, true, M_total, N, true, mm::BM) ||
       !mm::make_operand(&maps.b, A, true, M_total, K, true, 256 / pair) ||
-      !mm::make_boxes(&maps.c[0], dB, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      f32 ? 4 : 2, E, N, K, 64)) {
+      !mm::make_boxes(&maps.c[0], parts > 1 ? scratch : dB,
+                      wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wide ? 4 : 2,
+                      (int64_t)parts * E, N, K, 64)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -350,11 +493,20 @@ cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* o
     op.bm = mm::BM * CG;
     op.mt = (int)ceil_div(N, op.bm);
     op.nt = (int)ceil_div(K, op.kBN);
-    return mm::launch<decltype(op), CG>(maps, op, (int64_t)E * op.mt * op.nt, status, s);
+    op.parts = parts;
+    return mm::launch<decltype(op), CG>(maps, op, tiles * parts, status, s);
   };
   auto any = [&](auto op) {
     return pair == 2 ? go(op, std::integral_constant<int, 2>{}) : go(op, std::integral_constant<int, 1>{});
   };
+  if (parts > 1) {
+    cudaError_t e = any(mm::WeightGrad<true, false>{});
+    if (e != cudaSuccess) return e;
+    auto sum = f32 ? add ? mm::sum_weights_kernel<true, true> : mm::sum_weights_kernel<true, false>
+                   : mm::sum_weights_kernel<false, false>;
+    return mm::launch_overlapped(sum, dim3((unsigned)ceil_div(n / 4, 256)), 256, s,
+                                 static_cast<const float4*>(scratch), parts, n / 4, dB);
+  }
   return !f32 ? any(mm::WeightGrad<false, false>{})
               : add ? any(mm::WeightGrad<true, true>{}) : any(mm::WeightGrad<true, false>{});
 }

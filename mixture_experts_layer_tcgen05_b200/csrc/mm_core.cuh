@@ -562,8 +562,10 @@ inline bool make_boxes(CUtensorMap* m, const void* base, CUtensorMapDataType dt,
 
 // overlap: the kernel may start (its set-up, up to wait_for_previous_grid)
 // while the one ahead of it in the stream still runs.
+// (static: were `sized` shared between two copies of this library in a process,
+// only one of them would set its kernels' size)
 template <class Op, int CG>
-inline cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t* status, cudaStream_t s,
+static cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t* status, cudaStream_t s,
                           bool overlap = false) {
   using C = Cfg<Op, CG>;
   auto k = mm_kernel<Op, CG>;

@@ -226,6 +226,88 @@ def test_wgrad(counts, N, K, kind):
             assert (out.t[e] == 0).all()
 
 
+# few tiles and long sums: cut into parts where the workspace has room for them
+@pytest.mark.parametrize("room", [256, 1 << 20, 1 << 24])
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("counts,N,K", [([5], 4096, 128), ([0, 31, 2], 3200, 384), ([130, 1], 2048, 256)])
+def test_dgrad_in_parts(counts, N, K, act, room):
+    E, R, behind = len(counts), sum(counts), 9
+    M = R + behind
+    gen = _gen(N + room)
+    dC, B = _randn(gen, M, N), _randn(gen, E, N, K, std=0.05)
+    gated = ACTS[act] is not None
+    gu = _randn(gen, M, 2 * K, std=2.0) if gated else None
+    out = Guarded((M, 2 * K if gated else K), BF16, fill=0x7B)
+    h = Guarded((M, K), BF16, fill=0x7B) if gated else None
+    ws = Guarded((room,), torch.uint8, fill=0xFF)
+    ws.t[:256] = 0
+    before = out.t[R:].clone()
+    moe.moe_grouped_gemm_dgrad(dC, B, _offsets(counts), M, E, N, K, act, out.t, gu=gu, h=h.t if gated else None,
+                               ws=ws.t)
+    assert moe.moe_get_device_status(ws.t) == 0
+    assert out.intact() and ws.intact() and torch.equal(out.t[R:].view(torch.int16), before.view(torch.int16))
+    d, eps = rows64(dC[:R], B, counts)
+    if not gated:
+        within(out.t[:R], d, d.abs() * 2.0**-8 + eps, "dA")
+        return
+    g, u = gu[:R, :K].double(), gu[:R, K:].double()
+    a, da = act64(ACTS[act], g)
+    ref = torch.cat([d * u * da, d * a], 1)
+    tol = ref.abs() * 2.0**-8 + torch.cat([eps * (u * da).abs(), eps * a.abs()], 1) + 2.0**-18 * torch.cat(
+        [(1 + g.abs()) * (d * u).abs(), (1 + g.abs()) * (d * g).abs()], 1)
+    within(out.t[:R], ref, tol, "gated gradients")
+    assert h.intact()
+    within(h.t[:R], a * u, (a * u).abs() * 2.0**-8 + 2.0**-18 * (1 + g.abs()) * (g * u).abs(), "h")
+
+
+@pytest.mark.parametrize("room", [256, 1 << 20, 1 << 24])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "add"])
+@pytest.mark.parametrize("counts,N,K", [([2600], 128, 128), ([4100, 0], 256, 384), ([2055, 3, 7000], 384, 128)])
+def test_wgrad_in_parts(counts, N, K, kind, room):
+    E, R = len(counts), sum(counts)
+    M = R + 70
+    gen = _gen(R + room)
+    dC, A = _randn(gen, M, N), _randn(gen, M, K)
+    dC[R:], A[R:] = float("nan"), float("inf")
+    out = Guarded((E, N, K), BF16 if kind == "bf16" else torch.float32, fill=0x7B)
+    if kind == "add":
+        out.t.copy_(_randn(gen, E, N, K, dtype=torch.float32, std=3.0))
+    old = out.t.double()
+    ws = Guarded((room,), torch.uint8, fill=0xFF)
+    ws.t[:256] = 0
+    moe.moe_grouped_gemm_wgrad(dC, A, _offsets(counts), M, E, N, K,
+                               moe.MOE_GRAD_BF16 if kind == "bf16" else moe.MOE_GRAD_F32, kind == "add", out.t, ws=ws.t)
+    assert moe.moe_get_device_status(ws.t) == 0 and out.intact() and ws.intact()
+    d, eps = weights64(dC[:R], A[:R], counts)
+    d = d + old if kind == "add" else d
+    within(out.t, d, d.abs() * (2.0**-8 if kind == "bf16" else 2.0**-24) + eps, "dB")
+
+
+def test_inputs_and_outputs_inside_the_workspace():
+    """Rows that live in the workspace (as a forward leaves them) are not overwritten by partial sums."""
+    E, R, N, K = 1, 24, 4096, 128
+    gen = _gen(21)
+    dC, B = _randn(gen, R, N), _randn(gen, E, N, K, std=0.05)
+    ws = _ws(1 << 24)
+    inside = ws[1024:1024 + R * N * 2].view(BF16).view(R, N)
+    inside.copy_(dC)
+    want, got = (torch.empty(R, K, dtype=BF16, device="cuda") for _ in range(2))
+    moe.moe_grouped_gemm_dgrad(dC, B, _offsets([R]), R, E, N, K, 0, want, ws=_ws(256))
+    moe.moe_grouped_gemm_dgrad(inside, B, _offsets([R]), R, E, N, K, 0, got, ws=ws)
+    assert torch.equal(inside, dC) and torch.equal(want, got)
+    out = ws[1 << 22:(1 << 22) + R * K * 2].view(BF16).view(R, K)
+    moe.moe_grouped_gemm_dgrad(dC, B, _offsets([R]), R, E, N, K, 0, out, ws=ws)
+    assert torch.equal(out, want)
+    R, N = 4000, 128
+    dC, A = _randn(gen, R, N), _randn(gen, R, K)
+    inside = ws[1024:1024 + R * N * 2].view(BF16).view(R, N)
+    inside.copy_(dC)
+    want, got = (torch.empty(1, N, K, device="cuda") for _ in range(2))
+    moe.moe_grouped_gemm_wgrad(dC, A, _offsets([R]), R, 1, N, K, moe.MOE_GRAD_F32, 0, want, ws=_ws(256))
+    moe.moe_grouped_gemm_wgrad(inside, A, _offsets([R]), R, 1, N, K, moe.MOE_GRAD_F32, 0, got, ws=ws)
+    assert torch.equal(inside, dC) and torch.equal(want, got)
+
+
 def test_wgrad_long_sums_stay_precise():
     """16384 rows of one expert: the fp32 sum stays within 1e-5 of the result's norm."""
     R, N, K = 16384 + 13, 256, 256
