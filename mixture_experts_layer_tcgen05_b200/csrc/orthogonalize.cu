@@ -8,19 +8,23 @@
 // (the right-sided form is the left-sided one of the transpose; it needs no
 // transposed copy, since mm_core.cuh takes operands of either majorness).
 //
-// Numbers. X is held in fp32: a step multiplies a small singular value by up
-// to a (3.4445 in Muon's polynomial), so five of them multiply a rounding of X
-// that is not in X's own row and column space by almost 500. A bf16 or fp16 X
-// loses matrices of low rank that way (measured with fp16 X on a rank-4 256 x
-// 256 matrix: 7e-2 of the result's norm; bf16 X: 0.5). The operands of the
-// products, though, may be rounded: A and B multiply X from the side, and the
-// X inside the products only meets B, so their roundings turn X's singular
-// vectors by a rounding's size and are not multiplied up. They are fp16, whose
-// 11 bits cost 2e-4 to 2e-3 of the result's norm over spectra from white to
-// rank 4 (bf16 operands: 3e-3 to 1.4e-2), at the same MMA rate. fp16's range
-// holds because every operand is stored times s = 2^floor(log2(q) / 2): |X|_2
-// and |A|_2 stay near 1, so entries of X reach from 1 / sqrt(p q) to 1, and
-// those of A from 1 / (p sqrt(q)) to 1. The norm is summed in fp64.
+// Numbers. A step multiplies a small singular value by up to a (3.4445 in
+// Muon's polynomial), so five of them multiply a rounding of X that is not in
+// X's own row and column space by almost 500. A bf16 or fp16 X loses matrices of
+// low rank that way (measured with fp16 X on a rank-4 256 x 256 matrix: 7e-2 of
+// the result's norm; bf16 X: 0.5). X is therefore held in 32 bits, as the sum of
+// two fp16 halves (22 bits of it, so 500 roundings' worth stays below 1e-4),
+// because the upper half is also what the products read: an fp32 X beside its
+// fp16 copy moves 12 bytes an element and step, the halves 8 (measured: 32
+// matrices of 7168 x 2048 @H ms, 17.8 with fp32). The products read the upper
+// half alone: A and B multiply X from the side, and the X inside the products
+// only meets B, so their roundings turn X's singular vectors by a rounding's
+// size and are not multiplied up. fp16's 11 bits there cost 2e-4 to 2e-3 of the
+// result's norm over spectra from white to rank 4 (bf16 operands: 3e-3 to
+// 1.4e-2), at the same MMA rate. fp16's range holds because everything is stored
+// times s = 2^floor(log2(q) / 2): |X|_2 and |A|_2 stay near 1, so entries of X
+// reach from 1 / sqrt(p q) to 1, and those of A from 1 / (p sqrt(q)) to 1. The
+// norm is summed in fp64.
 //
 // Work per step and matrix: p^2 q MACs for A and p^3 for A^2, each symmetric
 // and computed for its upper tiles only (the epilogue stores a tile and its
@@ -34,9 +38,9 @@
 namespace moe {
 namespace mm {
 
-// One stack in flight: nb matrices. The buffers X (fp32 [nb, mp, np]), s X
-// (fp16, two of them in turn), s A and s (b A + c A^2) (fp16 [nb, pp, pp]) are
-// padded to multiples of 64 in both directions with zeros, which stay zero
+// One stack in flight: nb matrices. The halves of s X (fp16 [nb, mp, np]; the
+// upper ones in two buffers in turn), s A and s (b A + c A^2) (fp16 [nb, pp, pp])
+// are padded to multiples of 64 in both directions with zeros, which stay zero
 // through every step.
 struct Stack {
   int nb, rows, cols;    // the caller's matrices
@@ -49,6 +53,21 @@ struct Stack {
   bool from_g, last;     // the step reads G as its state; it is the last one
   bool vec;              // cols % 8 == 0: rows of g and out in 16-byte units
 };
+
+// Two values of s X as pairs of halves: hi rounded to nearest, lo the rest times
+// 2^11, which keeps it in fp16's normal range. join gives them back to 22 bits.
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn((x - f.x) * 2048.0f, (y - f.y) * 2048.0f);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ float2 join(uint32_t hi, uint32_t lo) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  return make_float2(fmaf(l.x, 1.0f / 2048.0f, h.x), fmaf(l.y, 1.0f / 2048.0f, h.y));
+}
 
 // The products of X with itself (kGram, kPart) or of A with itself (kPoly):
 // symmetric results, tiles on and above the diagonal.
@@ -184,7 +203,7 @@ template <bool LEFT, int SIDE>
 struct Apply {
   static constexpr bool kAMn = false, kBMn = LEFT, kTail = false;
   static constexpr int kBN = SIDE, kFmt = 0, kChunk = 0;
-  static constexpr int kStageWarp = 10 * 1024, kSharedInts = 0;
+  static constexpr int kStageWarp = 8192, kSharedInts = 0;
 
   Stack st;
   int nkb, mt, nt;
@@ -193,7 +212,9 @@ struct Apply {
   __device__ int total(const int32_t*) const { return st.nb * mt * nt; }
   __device__ void decode(const int32_t*, int tile, Tile& t) const {
     const int b = tile / (mt * nt), l = tile - b * (mt * nt);
-    const int m = (l % mt) * SIDE, n = (l / mt) * SIDE;
+    // neighbours share X's tile (and all of B comes from L2): the right-sided
+    // form walks B's columns first, the left-sided one its rows
+    const int m = (LEFT ? l % mt : l / nt) * SIDE, n = (LEFT ? l / mt : l % nt) * SIDE;
     t.p[0] = b;
     t.p[1] = m;
     t.p[2] = n;
@@ -204,16 +225,22 @@ struct Apply {
     t.nkb = nkb;
     t.tail = BK;
   }
-  // The staging: two boxes of 32 x 32 fp32, in which the old state arrives and
-  // from which the new one leaves, and one of 32 x 32 for s X or the result.
+  // The staging: two of 4 KB, each 32 x 32 of the old state (its two halves, or
+  // an fp32 G), which the halves of the new one, or the result, replace.
   __device__ int steps(const Tile& t, const Warp& w) const {
     if (w.row0(t.p[1]) >= st.mp) return 0;
     const int left = st.np - t.p[2] - w.half * (kBN / 2);
     return max(0, min(kBN / 2, left)) / 32;
   }
   __device__ void load_state(const Tile& t, Warp& w, int i) const {
-    w.load(i & 1, w.base + (i & 1) * 4096, &w.maps->c[0], t.p[2] + w.half * (kBN / 2) + 32 * i, w.row0(t.p[1]),
-           t.p[0], 4096);
+    const int col = t.p[2] + w.half * (kBN / 2) + 32 * i, row0 = w.row0(t.p[1]);
+    const uint32_t box = w.base + (i & 1) * 4096, bar = w.bar + 8 * (i & 1);
+    if (w.lane == 0) {
+      ptx::mbar_arrive_expect_tx(bar, 4096);
+      ptx::tma_load_3d(box, &w.maps->c[0], col, row0, t.p[0], bar);
+      if (!st.from_g) ptx::tma_load_3d(box + 2048, &w.maps->c[1], col, row0, t.p[0], bar);
+    }
+    w.pending |= 1u << (i & 1);
   }
   __device__ void prefetch(const Tile& t, Warp& w) const {
     if (steps(t, w) == 0) return;
@@ -222,56 +249,73 @@ struct Apply {
   }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
     const int row0 = w.row0(t.p[1]), row = row0 + w.lane, n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
-    const float f = st.inv_s * st.inv_s;
-    // the first step may read G itself, the others X
+    // v = s (a X + B X): the accumulator holds s^2 B X
     const float2 inv = st.from_g ? st.inv[t.p[0]] : make_float2(1.0f, 1.0f);
-    const float a = st.a * inv.y;
+    const float as = st.a * st.s * inv.y;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int col = col0 + 32 * i;
-      const uint32_t box = w.base + (i & 1) * 4096, hbox = w.base + 8192;
+      const uint32_t box = w.base + (i & 1) * 4096;
       w.free_boxes();
       if (i + 1 < n) load_state(t, w, i + 1);
       float v[32];
       load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
       if (!w.wait(i & 1)) return false;
+      if (st.from_g) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t at = Warp::at128(box, w.lane, j);
-        const uint4 x = Warp::get(at);
-        v[4 * j] = fmaf(a, inv.x * __uint_as_float(x.x), f * v[4 * j]);
-        v[4 * j + 1] = fmaf(a, inv.x * __uint_as_float(x.y), f * v[4 * j + 1]);
-        v[4 * j + 2] = fmaf(a, inv.x * __uint_as_float(x.z), f * v[4 * j + 2]);
-        v[4 * j + 3] = fmaf(a, inv.x * __uint_as_float(x.w), f * v[4 * j + 3]);
-        if (!st.last)
-          Warp::put(at, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                   __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
-      }
-      const float s = st.last ? st.scale : st.s;
-      if (st.last && !st.vec) {  // rows of the result that a tiled store cannot address
-        if (row < st.rows) {
-          __nv_bfloat16* dst = st.out + ((int64_t)t.p[0] * st.rows + row) * st.cols + col;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (col + j < st.cols) dst[j] = __float2bfloat16_rn(s * v[j]);
+        for (int j = 0; j < 8; ++j) {
+          const uint4 x = Warp::get(Warp::at128(box, w.lane, j));
+          v[4 * j] = fmaf(as, inv.x * __uint_as_float(x.x), st.inv_s * v[4 * j]);
+          v[4 * j + 1] = fmaf(as, inv.x * __uint_as_float(x.y), st.inv_s * v[4 * j + 1]);
+          v[4 * j + 2] = fmaf(as, inv.x * __uint_as_float(x.z), st.inv_s * v[4 * j + 2]);
+          v[4 * j + 3] = fmaf(as, inv.x * __uint_as_float(x.w), st.inv_s * v[4 * j + 3]);
         }
-        continue;
-      }
+        __syncwarp();  // every lane has its row of G: the box may take the halves
+      } else {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t o[4];
+        for (int u = 0; u < 4; ++u) {
+          const uint4 h = Warp::get(Warp::at64(box, w.lane, u)), l = Warp::get(Warp::at64(box + 2048, w.lane, u));
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = s * v[8 * u + 2 * j], hi = s * v[8 * u + 2 * j + 1];
-          const __half2 h = __floats2half2_rn(lo, hi);
-          o[j] = st.last ? pack_bf16x2(lo, hi) : *reinterpret_cast<const uint32_t*>(&h);
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = join(hw[j], lw[j]);
+            v[8 * u + 2 * j] = fmaf(st.a, x.x, st.inv_s * v[8 * u + 2 * j]);
+            v[8 * u + 2 * j + 1] = fmaf(st.a, x.y, st.inv_s * v[8 * u + 2 * j + 1]);
+          }
         }
-        Warp::put(Warp::at64(hbox, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      if (st.last) {
+        const float r = st.scale * st.inv_s;
+        if (!st.vec) {  // rows of the result that a tiled store cannot address
+          if (row < st.rows) {
+            __nv_bfloat16* dst = st.out + ((int64_t)t.p[0] * st.rows + row) * st.cols + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j < st.cols) dst[j] = __float2bfloat16_rn(r * v[j]);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(r * v[8 * u + 2 * j], r * v[8 * u + 2 * j + 1]);
+          Warp::put(Warp::at64(box, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t o[4], l[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) split(v[8 * u + 2 * j], v[8 * u + 2 * j + 1], o[j], l[j]);
+          Warp::put(Warp::at64(box, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
+          Warp::put(Warp::at64(box + 2048, w.lane, u), make_uint4(l[0], l[1], l[2], l[3]));
+        }
       }
       w.publish();
       if (w.lane == 0) {
-        if (!st.last) ptx::tma_store_3d(&w.maps->c[1], box, col, row0, t.p[0]);
-        ptx::tma_store_3d(&w.maps->c[2], hbox, col, row0, t.p[0]);
+        ptx::tma_store_3d(&w.maps->c[2], box, col, row0, t.p[0]);
+        if (!st.last) ptx::tma_store_3d(&w.maps->c[1], box + 2048, col, row0, t.p[0]);
         ptx::bulk_commit();
       }
     }
@@ -323,13 +367,12 @@ __global__ void __launch_bounds__(kNormThreads) sumsq_kernel(const T* __restrict
   if (threadIdx.x == 0) part[b * chunks + blockIdx.x] = s;
 }
 
-// xh = s G / (|G|_F + eps) in fp16, zero in the padding; inv[b] kept for a
-// first step that reads G as its state, else (x given) X = G / (|G|_F + eps) in
-// fp32 beside it.
+// The upper half of s G / (|G|_F + eps), zero in the padding; inv[b] kept for a
+// first step that reads G as its state, else (xl given) the lower half too.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const double* __restrict__ part,
                                                                  int chunks, float eps, float2* __restrict__ inv,
-                                                                 __half* __restrict__ xh, float* __restrict__ x32) {
+                                                                 __half* __restrict__ xh, __half* __restrict__ xl) {
   ptx::let_next_grid_start();
   ptx::wait_for_previous_grid();
   const int64_t b = blockIdx.y;
@@ -368,20 +411,12 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const
           if (col + j < st.cols) x[j] = (float)at[j];
       }
     }
-    uint32_t o[4];
+    uint32_t o[4], l[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = p * x[j] * r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(x[2 * j] * st.s, x[2 * j + 1] * st.s);
-      o[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+    for (int j = 0; j < 4; ++j) split(p * x[2 * j] * r * st.s, p * x[2 * j + 1] * r * st.s, o[j], l[j]);
     const int64_t at = base + (int64_t)row * st.np + col;
     *reinterpret_cast<uint4*>(xh + at) = make_uint4(o[0], o[1], o[2], o[3]);
-    if (x32) {
-      *reinterpret_cast<float4*>(x32 + at) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(x32 + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    }
+    if (xl) *reinterpret_cast<uint4*>(xl + at) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -441,7 +476,7 @@ inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
 
 struct OrthPlan {
   int64_t mp, np, pp, chunks;
-  int64_t part, inv, x, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
+  int64_t part, inv, xl, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
 };
 
 inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
@@ -458,7 +493,7 @@ inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
   };
   p.part = take(nb * p.chunks * 8);
   p.inv = take(nb * 8);
-  p.x = take(nb * p.mp * p.np * 4);
+  p.xl = take(nb * p.mp * p.np * 2);
   p.xh0 = take(nb * p.mp * p.np * 2);
   p.xh1 = take(nb * p.mp * p.np * 2);
   p.gram = take(nb * p.pp * p.pp * 2);
@@ -498,7 +533,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   st.g = g;
   st.vec = cols % 8 == 0;
   st.out = static_cast<__nv_bfloat16*>(out);
-  float* x32 = reinterpret_cast<float*>(ws + P.x);
+  __half* xl = reinterpret_cast<__half*>(ws + P.xl);
   void* gram = ws + P.gram;
   void* poly = ws + P.poly;
   float2* inv = reinterpret_cast<float2*>(ws + P.inv);
@@ -508,7 +543,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   int32_t* status = reinterpret_cast<int32_t*>(ws);
   // the first step reads an fp32 G whose rows tiled loads can address itself
   const bool g_state = g_f32 && cols % 4 == 0;
-  float* x_init = g_state ? nullptr : x32;
+  __half* xl_init = g_state ? nullptr : xl;
 
   const dim3 ngrid((unsigned)P.chunks, (unsigned)nb);
   const int64_t vecs = P.mp * P.np / 8;
@@ -520,7 +555,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
     e = launch_overlapped(sumsq_kernel<T>, ngrid, kNormThreads, s, static_cast<const T*>(g), n, (int)P.chunks, part);
     if (e == cudaSuccess)
       e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, st, (const double*)part, (int)P.chunks, eps,
-                            inv, xh[0], x_init);
+                            inv, xh[0], xl_init);
   };
   if (g_f32) norms(0.0f);
   else norms(__nv_bfloat16());
@@ -529,16 +564,16 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   const bool left = rows <= cols;
   const CUtensorMapDataType f32t = CU_TENSOR_MAP_DATA_TYPE_FLOAT32, f16t = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap xk[2], xmn[2], gk, pk;       // operands: X K-major and MN-major, A and B K-major
-  CUtensorMap g_in, x_io, xh_out[2], g_io, p_out, o_out = {};  // the epilogues' boxes
+  CUtensorMap g_in, xl_io, xh_io[2], g_io, p_out, o_out = {};  // the epilogues' boxes
   // MN rows of an operand in one CTA are 128 either way
   bool ok = make_operand(&gk, gram, false, nb * P.pp, P.pp, false, 128) &&
             make_operand(&pk, poly, false, nb * P.pp, P.pp, false, 128) &&
-            make_boxes(&x_io, x32, f32t, 4, nb, P.mp, P.np, 128) && make_boxes(&g_io, gram, f16t, 2, nb, P.pp, P.pp, 64) &&
+            make_boxes(&xl_io, xl, f16t, 2, nb, P.mp, P.np, 64) && make_boxes(&g_io, gram, f16t, 2, nb, P.pp, P.pp, 64) &&
             make_boxes(&p_out, poly, f16t, 2, nb, P.pp, P.pp, 64);
   for (int i = 0; i < 2; ++i)
     ok = ok && make_operand(&xk[i], xh[i], false, nb * P.mp, P.np, false, 128) &&
          make_operand(&xmn[i], xh[i], false, nb * P.mp, P.np, true, 128) &&
-         make_boxes(&xh_out[i], xh[i], f16t, 2, nb, P.mp, P.np, 64);
+         make_boxes(&xh_io[i], xh[i], f16t, 2, nb, P.mp, P.np, 64);
   if (g_state) ok = ok && make_boxes(&g_in, g, f32t, 4, nb, rows, cols, 128);
   if (st.vec) ok = ok && make_boxes(&o_out, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, nb, rows, cols, 64);
   if (!ok) {
@@ -583,7 +618,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       op.mt = (int)ceil_div(P.mp, SIDE);
       op.nt = (int)ceil_div(P.np, SIDE);
       const Maps maps = {LEFT ? pk : xk[in], LEFT ? xmn[in] : pk,
-                         {st.from_g ? g_in : x_io, x_io, st.last ? o_out : xh_out[in ^ 1]}};
+                         {st.from_g ? g_in : xh_io[in], xl_io, st.last ? o_out : xh_io[in ^ 1]}};
       e = launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s, true);
       if (e != cudaSuccess) return e;
     }

@@ -122,8 +122,8 @@ def test_orthogonalize_workspace_follows_its_bound(nb, rows, cols):
     n = moe.moe_orthogonalize_workspace_size(nb, rows, cols)
     p = min(rows, cols)
     assert 0 < n <= 65536 + nb * (12 * (rows + 127) * (cols + 127) + 8 * (p + 127) ** 2)
-    # the fp32 state and two fp16 copies of the stack, and two fp16 squares
-    assert n >= nb * (8 * rows * cols + 4 * p * p)
+    # the state's two halves, the upper one twice, and two squares, all fp16
+    assert n >= nb * (6 * rows * cols + 4 * p * p)
     assert moe.moe_orthogonalize_workspace_size(nb + 1, rows, cols) > n
     for bad in ((0, rows, cols), (nb, 0, cols), (nb, rows, (1 << 20) + 1)):
         assert moe.moe_orthogonalize_workspace_size(*bad) == 0
