@@ -449,7 +449,7 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
       cudaError_t e = go(mm::RowGrad<kActNone, false>{}, One{}, mm::kAllRows);
       if (e != cudaSuccess) return e;
       const dim3 grid((unsigned)ceil_div(M_total, 8), (unsigned)ceil_div(K, 1024));
-      return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, static_cast<const float*>(scratch), parts,
+      return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, 1, static_cast<const float*>(scratch), parts,
                                    offsets, E, M_total, K, static_cast<const __nv_bfloat16*>(gu),
                                    static_cast<__nv_bfloat16*>(dA), static_cast<__nv_bfloat16*>(h));
     }
@@ -504,7 +504,7 @@ cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* o
     if (e != cudaSuccess) return e;
     auto sum = f32 ? add ? mm::sum_weights_kernel<true, true> : mm::sum_weights_kernel<true, false>
                    : mm::sum_weights_kernel<false, false>;
-    return mm::launch_overlapped(sum, dim3((unsigned)ceil_div(n / 4, 256)), 256, s,
+    return mm::launch_overlapped(sum, dim3((unsigned)ceil_div(n / 4, 256)), 256, s, 1,
                                  static_cast<const float4*>(scratch), parts, n / 4, dB);
   }
   return !f32 ? any(mm::WeightGrad<false, false>{})

@@ -605,18 +605,23 @@ static cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t
   return cudaGetLastError();
 }
 
-// A plain kernel that starts with wait_for_previous_grid, launched to overlap.
+// A plain kernel that starts with wait_for_previous_grid, launched to overlap;
+// its blocks in clusters of `cluster`.
 template <typename... Par, typename... Arg>
-inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned threads, cudaStream_t s, Arg... args) {
+inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned threads, cudaStream_t s, unsigned cluster,
+                                     Arg... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
-  cudaLaunchAttribute at[1] = {};
+  cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, k, static_cast<Par>(args)...);
   if (e != cudaSuccess) return e;
   note_launch();

@@ -16,12 +16,14 @@
 // two fp16 halves (22 bits of it, so 500 roundings' worth stays below 1e-4),
 // because the upper half is also what the products read: an fp32 X beside its
 // fp16 copy moves 12 bytes an element and step, the halves 8 (measured: 32
-// matrices of 7168 x 2048 @H ms, 17.8 with fp32). The products read the upper
+// matrices of 7168 x 2048 16.9 ms, 18.3 with fp32). The products read the upper
 // half alone: A and B multiply X from the side, and the X inside the products
 // only meets B, so their roundings turn X's singular vectors by a rounding's
 // size and are not multiplied up. fp16's 11 bits there cost 2e-4 to 2e-3 of the
 // result's norm over spectra from white to rank 4 (bf16 operands: 3e-3 to
-// 1.4e-2), at the same MMA rate. fp16's range holds because everything is stored
+// 1.4e-2), at the same MMA rate. The largest part of that is the diagonal of
+// b A + c A^2, which nears b + c while the rest of it nears 0: what its rounding
+// takes is kept in fp32 and given back as a factor of X (a fifth to a third less). fp16's range holds because everything is stored
 // times s = 2^floor(log2(q) / 2): |X|_2 and |A|_2 stay near 1, so entries of X
 // reach from 1 / sqrt(p q) to 1, and those of A from 1 / (p sqrt(q)) to 1. The
 // norm is summed in fp64.
@@ -49,6 +51,7 @@ struct Stack {
   float a, b, c, scale;
   const void* g;         // [nb, rows, cols] fp32 or bf16
   const float2* inv;     // [nb] 1 / (|G|_F + eps) as a power of two and the rest
+  float* rest;           // [nb, pp] what rounding took from the diagonal of b A + c A^2
   __nv_bfloat16* out;    // [nb, rows, cols]
   bool from_g, last;     // the step reads G as its state; it is the last one
   bool vec;              // cols % 8 == 0: rows of g and out in 16-byte units
@@ -167,6 +170,13 @@ struct Square {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] *= st.inv_s;
       }
+      if (POLY && col == row0) {
+        float d = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == w.lane) d = v[j];
+        st.rest[(int64_t)t.p[0] * st.pp + row0 + w.lane] = (d - __half2float(__float2half_rn(d))) * st.inv_s;
+      }
       w.free_boxes();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -249,26 +259,27 @@ struct Apply {
   }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
     const int row0 = w.row0(t.p[1]), row = row0 + w.lane, n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
-    // v = s (a X + B X): the accumulator holds s^2 B X
+    // v = s (a X + B X): the accumulator holds s^2 B X, but for the rest of B's
+    // diagonal, which joins a: one of this row (LEFT), or one of each column
     const float2 inv = st.from_g ? st.inv[t.p[0]] : make_float2(1.0f, 1.0f);
-    const float as = st.a * st.s * inv.y;
+    const float* rest = st.rest + (int64_t)t.p[0] * st.pp;
+    const float a_row = LEFT && row < st.pp ? st.a + rest[row] : st.a;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int col = col0 + 32 * i;
       const uint32_t box = w.base + (i & 1) * 4096;
       w.free_boxes();
       if (i + 1 < n) load_state(t, w, i + 1);
-      float v[32];
+      float v[32], x[32];
       load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
       if (!w.wait(i & 1)) return false;
       if (st.from_g) {
+        const float f = st.s * inv.y;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint4 x = Warp::get(Warp::at128(box, w.lane, j));
-          v[4 * j] = fmaf(as, inv.x * __uint_as_float(x.x), st.inv_s * v[4 * j]);
-          v[4 * j + 1] = fmaf(as, inv.x * __uint_as_float(x.y), st.inv_s * v[4 * j + 1]);
-          v[4 * j + 2] = fmaf(as, inv.x * __uint_as_float(x.z), st.inv_s * v[4 * j + 2]);
-          v[4 * j + 3] = fmaf(as, inv.x * __uint_as_float(x.w), st.inv_s * v[4 * j + 3]);
+          const uint4 g = Warp::get(Warp::at128(box, w.lane, j));
+          x[4 * j] = inv.x * __uint_as_float(g.x) * f, x[4 * j + 1] = inv.x * __uint_as_float(g.y) * f;
+          x[4 * j + 2] = inv.x * __uint_as_float(g.z) * f, x[4 * j + 3] = inv.x * __uint_as_float(g.w) * f;
         }
         __syncwarp();  // every lane has its row of G: the box may take the halves
       } else {
@@ -278,11 +289,22 @@ struct Apply {
           const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 x = join(hw[j], lw[j]);
-            v[8 * u + 2 * j] = fmaf(st.a, x.x, st.inv_s * v[8 * u + 2 * j]);
-            v[8 * u + 2 * j + 1] = fmaf(st.a, x.y, st.inv_s * v[8 * u + 2 * j + 1]);
+            const float2 y = join(hw[j], lw[j]);
+            x[8 * u + 2 * j] = y.x, x[8 * u + 2 * j + 1] = y.y;
           }
         }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float4 d = make_float4(a_row, a_row, a_row, a_row);
+        if constexpr (!LEFT) {
+          const float4 r = __ldg(reinterpret_cast<const float4*>(rest + col) + j);
+          d.x += r.x, d.y += r.y, d.z += r.z, d.w += r.w;
+        }
+        v[4 * j] = fmaf(d.x, x[4 * j], st.inv_s * v[4 * j]);
+        v[4 * j + 1] = fmaf(d.y, x[4 * j + 1], st.inv_s * v[4 * j + 1]);
+        v[4 * j + 2] = fmaf(d.z, x[4 * j + 2], st.inv_s * v[4 * j + 2]);
+        v[4 * j + 3] = fmaf(d.w, x[4 * j + 3], st.inv_s * v[4 * j + 3]);
       }
       if (st.last) {
         const float r = st.scale * st.inv_s;
@@ -474,9 +496,169 @@ inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
   return std::max<int64_t>(1, std::min({units / nb, nkb / 4, mp * np / (pp * pp)}));
 }
 
+// Narrow matrices, p <= 8: every step in one launch and in fp32 on the FMA
+// units. With so few rows a 64-wide MMA tile is mostly padding, the chain of
+// launches is most of the time, and the roundings of A and B have too few
+// elements to average out over (3 x 3, six steps: 4e-3 of the result's norm in
+// fp16 operands, 1e-6 here). The matrix is q vectors of p numbers, x [q, P] in
+// the workspace, P = p rounded up to a power of two, dealt to the threads of one
+// block or a cluster of eight. A pass over them takes a step's y = a x + B x and
+// sums y y^T, the next step's A; the cluster's blocks read each other's sums and
+// add them in the same order. Bound by the latency of a pass's loads.
+// Measured, against the MMA tiles: 4 x 4096 17 and 99 us, 16384 x 8 59 and 141,
+// 300 of 400 x 8 64 and 262, 8 x 300000 678 and 631.
+constexpr int kNarrow = 8, kNarrowThreads = 512, kNarrowCluster = 8;
+inline bool narrow(int64_t rows, int64_t cols) { return std::min(rows, cols) <= kNarrow; }
+
+template <int P>
+__device__ __forceinline__ void load_vector(const float* src, float (&v)[P]) {
+  if constexpr (P == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(src);
+    v[0] = x.x, v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < P / 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(src)[i];
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  }
+}
+
+template <int P, int CLUSTER>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+    narrow_kernel(const void* __restrict__ g, bool g_f32, int p, int q, bool wide, int steps, float a, float b, float c,
+                  float eps, float scale, float* xs, __nv_bfloat16* __restrict__ out) {
+  constexpr int PAIRS = P * (P + 1) / 2, WARPS = kNarrowThreads / 32, THREADS = kNarrowThreads * CLUSTER;
+  __shared__ double norms[WARPS], norm_of;
+  __shared__ float part[WARPS][PAIRS], sum[PAIRS], A[P][P], B[P][P];
+  ptx::let_next_grid_start();
+  ptx::wait_for_previous_grid();
+  const int item = (int)blockIdx.x / CLUSTER, rank = (int)blockIdx.x % CLUSTER;
+  const int64_t at = (int64_t)item * p * q;
+  const int64_t sp = wide ? q : 1, sq = wide ? 1 : p;  // strides of the short and the long axis
+  float* x = xs + (int64_t)item * q * P;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = rank * kNarrowThreads + threadIdx.x;
+  auto load = [&](int r, int j) {
+    const int64_t i = at + r * sp + j * sq;
+    return g_f32 ? __ldg(static_cast<const float*>(g) + i)
+                 : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(g) + i));
+  };
+  // another block's shared memory, read between two cluster barriers
+  auto peer_f32 = [](const float* v, int r) {
+    float o;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(ptx::map_to_cta(ptx::smem_addr(v), r)) : "memory");
+    return o;
+  };
+  auto peer_f64 = [](const double* v, int r) {
+    double o;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(o) : "r"(ptx::map_to_cta(ptx::smem_addr(v), r)) : "memory");
+    return o;
+  };
+  auto sync = [] {
+    if constexpr (CLUSTER > 1) ptx::cluster_sync();
+    else __syncthreads();
+  };
+  double s = 0.0;
+  for (int j = first; j < q; j += THREADS)
+#pragma unroll
+    for (int r = 0; r < P; ++r)
+      if (r < p) {
+        const double v = load(r, j);
+        s += v * v;
+      }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) norms[warp] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int u = 0; u < WARPS; ++u) s += norms[u];
+    norm_of = s;
+  }
+  sync();
+  s = 0.0;
+  for (int r = 0; r < CLUSTER; ++r) s += CLUSTER > 1 ? peer_f64(&norm_of, r) : norm_of;
+  const double norm = sqrt(s);
+  const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
+  const float f = (float)p2, inv = (float)(1.0 / (norm * p2 + (double)eps * p2));
+
+  // step -1 takes G; step i < steps - 1 leaves A of the one after it
+#pragma unroll 1
+  for (int step = -1; step < steps; ++step) {
+    float acc[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) acc[i] = 0.0f;
+#pragma unroll 2
+    for (int j = first; j < q; j += THREADS) {
+      float y[P];
+      if (step < 0) {
+#pragma unroll
+        for (int r = 0; r < P; ++r) y[r] = r < p ? f * load(r, j) * inv : 0.0f;
+      } else {
+        float v[P];
+        load_vector<P>(x + (int64_t)j * P, v);
+#pragma unroll
+        for (int r = 0; r < P; ++r) {
+          y[r] = a * v[r];
+#pragma unroll
+          for (int k = 0; k < P; ++k) y[r] = fmaf(B[r][k], v[k], y[r]);
+        }
+      }
+      if (step == steps - 1) {
+#pragma unroll
+        for (int r = 0; r < P; ++r)
+          if (r < p) out[at + r * sp + j * sq] = __float2bfloat16_rn(scale * y[r]);
+      } else {
+        int i = 0;
+#pragma unroll
+        for (int r = 0; r < P; ++r) {
+          x[(int64_t)j * P + r] = y[r];
+#pragma unroll
+          for (int k = 0; k <= r; ++k) {
+            acc[i] = fmaf(y[r], y[k], acc[i]);
+            ++i;
+          }
+        }
+      }
+    }
+    if (step == steps - 1) break;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      if (lane == 0) part[warp][i] = acc[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < PAIRS) {
+      float v = 0.0f;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) v += part[u][threadIdx.x];
+      sum[threadIdx.x] = v;
+    }
+    sync();
+    if (threadIdx.x < P * P) {
+      const int r = threadIdx.x / P, k = threadIdx.x % P, i = r >= k ? r * (r + 1) / 2 + k : k * (k + 1) / 2 + r;
+      float v = 0.0f;
+#pragma unroll
+      for (int u = 0; u < CLUSTER; ++u) v += CLUSTER > 1 ? peer_f32(&sum[i], u) : sum[i];
+      A[r][k] = v;
+    }
+    sync();  // (the others have read `sum` too)
+    if (threadIdx.x < P * P) {
+      const int r = threadIdx.x / P, k = threadIdx.x % P;
+      float v = 0.0f;
+#pragma unroll
+      for (int u = 0; u < P; ++u) v = fmaf(A[r][u], A[u][k], v);
+      B[r][k] = fmaf(b, A[r][k], c * v);
+    }
+    __syncthreads();
+  }
+  // (the last peer reads are behind a barrier of every step; with steps >= 1 there was one)
+}
+
 struct OrthPlan {
   int64_t mp, np, pp, chunks;
-  int64_t part, inv, xl, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
+  int64_t part, inv, rest, xl, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
 };
 
 inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
@@ -493,6 +675,7 @@ inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
   };
   p.part = take(nb * p.chunks * 8);
   p.inv = take(nb * 8);
+  p.rest = take(nb * p.pp * 4);
   p.xl = take(nb * p.mp * p.np * 2);
   p.xh0 = take(nb * p.mp * p.np * 2);
   p.xh1 = take(nb * p.mp * p.np * 2);
@@ -538,6 +721,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   void* poly = ws + P.poly;
   float2* inv = reinterpret_cast<float2*>(ws + P.inv);
   st.inv = inv;
+  st.rest = reinterpret_cast<float*>(ws + P.rest);
   double* part = reinterpret_cast<double*>(ws + P.part);
   __half* xh[2] = {reinterpret_cast<__half*>(ws + P.xh0), reinterpret_cast<__half*>(ws + P.xh1)};
   int32_t* status = reinterpret_cast<int32_t*>(ws);
@@ -545,6 +729,22 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   const bool g_state = g_f32 && cols % 4 == 0;
   __half* xl_init = g_state ? nullptr : xl;
 
+  if (narrow(rows, cols)) {
+    const int p = std::min(rows, cols), q = std::max(rows, cols);
+    auto run = [&](auto pc, auto cc) {
+      constexpr int PP = decltype(pc)::value, CLUSTER = decltype(cc)::value;
+      return launch_overlapped(narrow_kernel<PP, CLUSTER>, dim3((unsigned)(nb * CLUSTER)), kNarrowThreads, s, CLUSTER, g,
+                               g_f32, p, q, rows <= cols, steps, a, b, c, eps, scale,
+                               reinterpret_cast<float*>(ws + P.xl), st.out);
+    };
+    auto sized = [&](auto pc) {
+      return q >= 2 * kNarrowThreads ? run(pc, std::integral_constant<int, kNarrowCluster>{})
+                                     : run(pc, std::integral_constant<int, 1>{});
+    };
+    if (p <= 2) return sized(std::integral_constant<int, 2>{});
+    if (p <= 4) return sized(std::integral_constant<int, 4>{});
+    return sized(std::integral_constant<int, 8>{});
+  }
   const dim3 ngrid((unsigned)P.chunks, (unsigned)nb);
   const int64_t vecs = P.mp * P.np / 8;
   const dim3 cgrid((unsigned)std::min<int64_t>(1024, ceil_div(vecs, 4 * kNormThreads)), (unsigned)nb);
@@ -552,9 +752,9 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   cudaError_t e = cudaSuccess;
   auto norms = [&](auto zero) {
     using T = decltype(zero);
-    e = launch_overlapped(sumsq_kernel<T>, ngrid, kNormThreads, s, static_cast<const T*>(g), n, (int)P.chunks, part);
+    e = launch_overlapped(sumsq_kernel<T>, ngrid, kNormThreads, s, 1, static_cast<const T*>(g), n, (int)P.chunks, part);
     if (e == cudaSuccess)
-      e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, st, (const double*)part, (int)P.chunks, eps,
+      e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, 1, st, (const double*)part, (int)P.chunks, eps,
                             inv, xh[0], xl_init);
   };
   if (g_f32) norms(0.0f);
@@ -608,7 +808,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       cudaError_t e = parts == 1 ? square(Square<MN, kGram, SIDE>{}, x, k, P.mp, g_io, 1)
                                  : square(Square<MN, kPart, SIDE>{}, x, k, P.mp, sums_out, parts);
       if (e == cudaSuccess && parts > 1)
-        e = launch_overlapped(sum_parts_kernel, dim3((unsigned)((P.pp / 32) * (P.pp / 32)), (unsigned)nb), 256, s,
+        e = launch_overlapped(sum_parts_kernel, dim3((unsigned)((P.pp / 32) * (P.pp / 32)), (unsigned)nb), 256, s, 1,
                               (const float*)sums, parts, nb, (int)P.pp, SIDE, st.inv_s, reinterpret_cast<__half*>(gram));
       if (e == cudaSuccess) e = square(Square<false, kPoly, SIDE>{}, gk, P.pp, P.pp, p_out, 1);
       if (e != cudaSuccess) return e;

@@ -461,7 +461,8 @@ def check_orth(got, ref, steps):
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 @pytest.mark.parametrize("nb,rows,cols", [(1, 1, 1), (1, 1, 7), (2, 9, 1), (2, 5, 3), (1, 64, 64), (3, 65, 130),
                                           (2, 130, 65), (2, 128, 384), (2, 384, 128), (1, 257, 1000), (1, 1000, 257),
-                                          (1, 320, 320), (5, 40, 72), (1, 2000, 24), (2, 513, 769)])
+                                          (1, 320, 320), (5, 40, 72), (1, 2000, 24), (2, 513, 769), (3, 4, 4),
+                                          (2, 7, 1024), (2, 1023, 8), (1, 9, 1500), (2, 3000, 5), (3, 6, 9001), (150, 2, 3)])
 def test_orthogonalize(nb, rows, cols, dtype):
     G = _randn(_gen(rows * 3 + cols), nb, rows, cols, dtype=dtype)
     check_orth(orth(G), newton64(G, 5), 5)
