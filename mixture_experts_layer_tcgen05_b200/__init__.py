@@ -149,6 +149,25 @@ def _p(a):
     raise TypeError(f"cannot take the address of {type(a)}")
 
 
+def _ts(*args):
+    """Addresses of dense tensors on the current device / ints / None: what a kernel there may read or write."""
+    current, out = None, []
+    for a in args:
+        if a is not None and not isinstance(a, int):
+            device = a.get_device()
+            if current is None and device >= 0:
+                import torch
+                current = torch.cuda.current_device()
+            if device < 0 or device != current:
+                raise MoeError(MOE_ERR_INVALID_ARG, f"a tensor is on {a.device}, not on the current CUDA device")
+            if not a.is_contiguous():
+                raise MoeError(MOE_ERR_INVALID_ARG, f"a tensor of shape {tuple(a.shape)} has strides {a.stride()}: "
+                                                    "it must be dense and row-major")
+            a = a.data_ptr()
+        out.append(a)
+    return out
+
+
 def _s(stream):
     if stream is None:
         import torch
@@ -345,21 +364,21 @@ def moe_ep_return(y_loc, plan, E, G, cap_rows, row_bytes, src_bufs, src_rows, ws
 
 def moe_grouped_gemm_dgrad(dC, B, offsets, M_total, E, N, K, ep, dA, gu=None, h=None,
                            max_rows_per_expert=0, ws=None, ws_bytes=None, stream=None):
-    _check(lib().moe_grouped_gemm_dgrad(_p(dC), _p(B), _p(offsets), M_total, E, N, K, int(ep),
-                                        _p(gu), _p(dA), _p(h), int(max_rows_per_expert), _p(ws),
-                                        _nbytes(ws, ws_bytes), _s(stream)))
+    pdC, pB, po, pgu, pdA, ph, pws = _ts(dC, B, offsets, gu, dA, h, ws)
+    _check(lib().moe_grouped_gemm_dgrad(pdC, pB, po, M_total, E, N, K, ep, pgu, pdA, ph,
+                                        max_rows_per_expert, pws, _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def moe_grouped_gemm_wgrad(dC, A, offsets, M_total, E, N, K, type, accumulate, dB, ws=None,
                            ws_bytes=None, stream=None):
-    _check(lib().moe_grouped_gemm_wgrad(_p(dC), _p(A), _p(offsets), M_total, E, N, K, int(type),
-                                        int(bool(accumulate)), _p(dB), _p(ws),
-                                        _nbytes(ws, ws_bytes), _s(stream)))
+    pdC, pA, po, pdB, pws = _ts(dC, A, offsets, dB, ws)
+    _check(lib().moe_grouped_gemm_wgrad(pdC, pA, po, M_total, E, N, K, type, bool(accumulate), pdB,
+                                        pws, _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def moe_combine_backward(dout, y_perm, w, inv_perm, d, dy_perm, dw, ws=None, stream=None):
-    _check(lib().moe_combine_backward(_p(dout), _p(y_perm), _p(w), _p(inv_perm), _dims(d),
-                                      _p(dy_perm), _p(dw), _p(ws), _s(stream)))
+    pdo, py, pw, pi, pdy, pdw, pws = _ts(dout, y_perm, w, inv_perm, dy_perm, dw, ws)
+    _check(lib().moe_combine_backward(pdo, py, pw, pi, _dims(d), pdy, pdw, pws, _s(stream)))
 
 
 def moe_orthogonalize_workspace_size(nb, rows, cols) -> int:
@@ -370,8 +389,9 @@ def moe_orthogonalize(g, nb, rows, cols, g_type, steps, coeffs, eps, scale, out,
                       stream=None):
     """coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
     a, b, c = coeffs
-    _check(lib().moe_orthogonalize(_p(g), nb, rows, cols, int(g_type), int(steps), a, b, c, eps,
-                                   scale, _p(out), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
+    pg, po, pws = _ts(g, out, ws)
+    _check(lib().moe_orthogonalize(pg, nb, rows, cols, g_type, steps, a, b, c, eps, scale, po, pws,
+                                   _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def moe_get_device_status(ws) -> int:

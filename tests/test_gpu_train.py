@@ -371,6 +371,14 @@ def test_offsets_out_of_range_write_nothing_else():
         within(dB.t[e:e + 1], d, d.abs() * 2.0**-24 + s, "dB")
 
 
+def test_binding_refuses_strided_tensors():
+    dC, B, dA = (torch.zeros(128, 256, dtype=BF16, device="cuda") for _ in range(3))
+    for kw in (dict(dC=dC.t()), dict(B=B[:, ::2]), dict(dA=dA.t())):
+        a = dict(dC=dC, B=B, offsets=_offsets([128]), M_total=128, E=1, N=128, K=128, ep=0, dA=dA, ws=_ws(256)) | kw
+        with pytest.raises(moe.MoeError, match="dense"):
+            moe.moe_grouped_gemm_dgrad(**a)
+
+
 # ------------------------------------------------------------------ combine
 @pytest.mark.parametrize("T,H,k", [(1, 128, 1), (1, 128, 2), (3, 256, 3), (16, 4096, 2), (33, 1152, 4), (7, 7168, 8),
                                    (5, 384, 9), (64, 128, 16), (300, 640, 6)])

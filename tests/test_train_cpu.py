@@ -127,3 +127,11 @@ def test_orthogonalize_workspace_follows_its_bound(nb, rows, cols):
     assert moe.moe_orthogonalize_workspace_size(nb + 1, rows, cols) > n
     for bad in ((0, rows, cols), (nb, 0, cols), (nb, rows, (1 << 20) + 1)):
         assert moe.moe_orthogonalize_workspace_size(*bad) == 0
+
+
+def test_binding_refuses_tensors_elsewhere():
+    """A CPU tensor's address is no device pointer."""
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(64, 256, dtype=torch.bfloat16)
+    for call in (dgrad(dC=t), wgrad(A=t), combine(dout=t), orth(g=t)):
+        refused(call, INV, "current CUDA device")
