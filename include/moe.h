@@ -2,7 +2,8 @@
  * moe.h -- C ABI of the B200 (sm_100a) sparse Mixture-of-Experts FFN layer
  * forward: router -> softmax top-k -> permutation by expert -> grouped
  * gated-MLP GEMMs (gate/up, SwiGLU, down) -> weighted combine, in bf16 and in
- * fine-grained FP8.
+ * fine-grained FP8; and, in bf16, the gradients of the grouped GEMMs and of the
+ * combine, and orthogonalised updates of the experts' weights.
  *
  * Passages the operations follow (titles of the pages they come from):
  *   [R]  "Mixture of Experts (MoE): a practical explanation of how expert
@@ -396,12 +397,17 @@ typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
  *   gu_dev bf16 [M_total, 2K] (gated: g, then u, per row), else NULL
  *   dA_dev bf16 [M_total, K], gated [M_total, 2K]
  *   h_dev  bf16 [M_total, K] or NULL (gated), else NULL
- *   max_rows_per_expert as in moe_grouped_gemm (0 = unknown); bounds <= 64
- *          select the small-M variant. More rows than the bound are not an error.
- * N, K multiples of 128, E*N < 2^31. Accumulation is fp32; every output is
- * rounded once. Offsets are clamped to [0, M_total]; rows of no expert are left
- * as they were. Outputs overlap nothing. ws: as in moe_grouped_gemm; calls that
- * may run at the same time need a workspace each. */
+ *   max_rows_per_expert: a bound on any expert's rows (0 = unknown); bounds <=
+ *          128 save a launch. More rows than the bound are not an error.
+ * N, K multiples of 128 up to 2^24, E*N < 2^31. Accumulation is fp32; every
+ * output is rounded once. Offsets are clamped to [0, M_total]; rows of no expert
+ * are left as they were. Outputs overlap neither inputs nor each other.
+ *   ws: its first 256 bytes hold the status word (zero before the first use),
+ *       the rest may take fp32 partial sums of long sums over few tiles; the sum's
+ *       order, and so its last bits, depend on how many fit. Inputs and outputs
+ *       may lie in the workspace past its first 256 bytes (then it takes no
+ *       partial sums). Calls that may run at the same time, captured graphs
+ *       included, need a workspace each. */
 moe_status_t moe_grouped_gemm_dgrad(const void* dC_dev, const void* B_dev, const int32_t* offsets_dev,
                                     int32_t M_total, int32_t E, int32_t N, int32_t K,
                                     moe_epilogue_t ep, const void* gu_dev, void* dA_dev, void* h_dev,
@@ -413,7 +419,7 @@ moe_status_t moe_grouped_gemm_dgrad(const void* dC_dev, const void* B_dev, const
  *   dC_dev bf16 [M_total, N], A_dev bf16 [M_total, K]
  *   dB_dev [E, N, K] of `type`; an expert without rows gets zeros
  *   accumulate != 0: added to what dB holds (fp32 only; an expert without rows
- *          keeps its values)
+ *          keeps its values; sums below fp32's smallest normal may become zero)
  * Dimensions, offsets, workspace and overlap as for moe_grouped_gemm_dgrad.
  * Sums are fp32, in an order that does not change from run to run. */
 moe_status_t moe_grouped_gemm_wgrad(const void* dC_dev, const void* A_dev, const int32_t* offsets_dev,
@@ -444,12 +450,17 @@ moe_status_t moe_combine_backward(const void* dout_dev, const void* y_perm_dev, 
  *   steps in [1, 64]; Muon's polynomial is a = 3.4445, b = -4.7750, c = 2.0315, 5 steps
  *   ws      at least moe_orthogonalize_workspace_size(1, rows, cols) bytes;
  *           with moe_orthogonalize_workspace_size(nb, ...) the whole stack
- *           runs at once, with less in as many passes as it takes
- * Any rows and cols in [1, 2^20]. The state X is fp32; the products take fp16
- * operands (scaled so that |X|_2 about 1, which the norm and a polynomial with
- * bounded steps give, fits) and accumulate in fp32. A polynomial that lets |X|_2
- * grow past some hundreds gives Inf or NaN. A zero matrix gives zeros for eps >
- * 0; NaN or Inf in one matrix do not reach another. Nothing may overlap. */
+ *           runs at once, with less in as many passes as it takes, to the same
+ *           bits. Its first 256 bytes hold the status word (zero before the first
+ *           use). Calls that may run at the same time, captured graphs included,
+ *           need a workspace each.
+ * Any rows and cols in [1, 2^20], nb * (rows + 63) < 2^31. The state X is held in
+ * two fp16 halves (22 bits); the products take the upper half (scaled so that
+ * |X|_2 about 1, which the norm and a polynomial with bounded steps give, fits)
+ * and accumulate in fp32; matrices with at most 8 rows or columns are computed in
+ * fp32. A polynomial that lets |X|_2 grow past some hundreds gives Inf or NaN. A
+ * zero matrix gives zeros for eps > 0; NaN or Inf in one matrix do not reach
+ * another. Nothing may overlap. */
 moe_status_t moe_orthogonalize(const void* g_dev, int32_t nb, int32_t rows, int32_t cols,
                                moe_grad_type_t g_type, int32_t steps, float a, float b, float c,
                                float eps, float scale, void* out_dev, void* ws, size_t ws_bytes,

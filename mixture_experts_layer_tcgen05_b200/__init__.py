@@ -1,4 +1,4 @@
-"""B200 (sm_100a) sparse Mixture-of-Experts FFN layer forward.
+"""B200 (sm_100a) sparse Mixture-of-Experts FFN layer: forward, gradients, weight updates.
 
 A thin ctypes binding of ``libmoe_b200.so`` (the C ABI in ``include/moe.h``):
 every function here has the C entry point's name and arguments and only
@@ -10,7 +10,8 @@ or ``__graft_entry__.build()``).
 
 Arguments that are device buffers accept a ``torch.Tensor`` (its
 ``data_ptr()``), a raw integer address, or ``None`` where the C function
-allows NULL. ``stream`` defaults to torch's current CUDA stream.
+allows NULL; the training entries refuse tensors that are strided or not on
+the current device. ``stream`` defaults to torch's current CUDA stream.
 """
 from __future__ import annotations
 
