@@ -573,8 +573,10 @@ moe_status_t moe_ep_return(const void* y_loc_dev, const int32_t* plan_dev, int32
  * GEMM producer waiting for a free stage, 2 an MMA thread waiting for its
  * operands, 3 an MMA thread waiting for a free accumulator, 4 an epilogue
  * waiting for a full accumulator, 5 the final drain, 7 the self-test below,
- * 8 a row load of the row scatter; code MOE_ERR_INVALID_ARG with site 6 means
- * an expert id or row index out of range was met and skipped. Synchronises
+ * 8 a row load of the row scatter, 9 the zeroing of a ragged sum's last rows
+ * waiting for them, 10 an epilogue waiting for its own loads; code
+ * MOE_ERR_INVALID_ARG with site 6 means an expert id or row index out of range
+ * was met and skipped. Synchronises
  * the device (a blocking copy); not for hot loops. */
 moe_status_t moe_get_device_status(const void* ws, int32_t* status_out);
 

@@ -520,14 +520,16 @@ moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t
   const uint64_t M = (uint64_t)M_total, out = M * K * 2 * (ep == MOE_EPILOGUE_NONE ? 1 : 2);
   const struct { const void* p; uint64_t n; const char* name; } in[] = {
       {dC, M * N * 2, "dC"}, {B, (uint64_t)E * N * K * 2, "B"}, {gu, M * K * 4, "gu"},
-      {offsets, (uint64_t)(E + 1) * 4, "expert_offsets"}, {ws, 256, "ws"}};
-  bool scratch = true;  // buffers that live in the workspace themselves leave no room for partial sums in it
+      {offsets, (uint64_t)(E + 1) * 4, "expert_offsets"}};
+  // buffers that live in the workspace themselves leave no room for partial sums in it
+  bool scratch = !overlaps(ws, ws_bytes, dA, out) && !overlaps(ws, ws_bytes, h, M * K * 2);
   for (const auto& i : in) {
     if (overlaps(dA, out, i.p, i.n) || overlaps(h, M * K * 2, i.p, i.n))
       return fail(MOE_ERR_INVALID_ARG, "an output overlaps %s", i.name);
-    scratch &= i.p == ws || !overlaps(ws, ws_bytes, i.p, i.n);
+    scratch &= !overlaps(ws, ws_bytes, i.p, i.n);
   }
-  scratch &= !overlaps(ws, ws_bytes, dA, out) && !overlaps(ws, ws_bytes, h, M * K * 2);
+  if (overlaps(dA, out, ws, 256) || overlaps(h, M * K * 2, ws, 256))
+    return fail(MOE_ERR_INVALID_ARG, "an output overlaps ws");
   if (overlaps(dA, out, h, M * K * 2)) return fail(MOE_ERR_INVALID_ARG, "dA and h overlap");
   MOE_TRY(check_device());
   const char* why = "";
@@ -553,12 +555,12 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dC, const void* A, const int32_t
   if (ws_bytes < 256) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes", ws_bytes);
   const uint64_t M = (uint64_t)M_total, out = (uint64_t)E * N * K * (type == MOE_GRAD_F32 ? 4 : 2);
   const struct { const void* p; uint64_t n; } in[] = {
-      {dC, M * N * 2}, {A, M * K * 2}, {offsets, (uint64_t)(E + 1) * 4}, {ws, 256}};
+      {dC, M * N * 2}, {A, M * K * 2}, {offsets, (uint64_t)(E + 1) * 4}};
   bool scratch = !overlaps(ws, ws_bytes, dB, out);  // as in moe_grouped_gemm_dgrad
-  bool clash = false;
+  bool clash = overlaps(dB, out, ws, 256);
   for (const auto& i : in) {
     clash |= overlaps(dB, out, i.p, i.n);
-    scratch &= i.p == ws || !overlaps(ws, ws_bytes, i.p, i.n);
+    scratch &= !overlaps(ws, ws_bytes, i.p, i.n);
   }
   if (clash)
     return fail(MOE_ERR_INVALID_ARG, "dB overlaps an input or the workspace");

@@ -176,7 +176,7 @@ struct RowGrad {
         if (ACT != kActNone && i + 1 < n) load_gu(t, w, i + 1);
       }
       float d[32];
-      load_acc32(taddr + c, false, d);
+      load_acc32(taddr + c, d);
       if constexpr (ACT == kActNone) {
         if (boxed) {
           put_row(w.base, w.lane, d);

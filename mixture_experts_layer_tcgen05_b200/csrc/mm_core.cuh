@@ -15,8 +15,7 @@
 //    step with valid rows, after the loads have landed and before the MMA;
 //  * CTA pairs (CG = 2): a tile is 256 x BN over two SMs, each holding 128
 //    rows of A and BN / 2 rows of B, so an SM streams 32 KB per k block instead
-//    of 48 KB for the same MMA time.
-//
+//    of 48 KB for the same MMA time;
 //  * sums of any length in fp32: the MMA truncates its running sum at every
 //    16-row step (measured: 1.9e-5 of the result's norm after 16397 rows, in
 //    proportion to the steps), so an Op that asks for it (kChunk) has every
@@ -69,7 +68,7 @@ struct Tile {
   int b_mn, b_k;
   int nkb;        // k blocks; 0: the accumulator is zero and is not read
   int tail;       // valid k rows of the last block (1..64)
-  int p[4];       // the Op's own
+  int p[3];       // the Op's own
 };
 
 template <class Op, int CG>
@@ -82,8 +81,7 @@ struct Cfg {
   static constexpr int kStageOut = Op::kStageWarp * kEpiWarps;
   static constexpr int kRest = 1024 + kStageOut + kBarBytes + Op::kSharedInts * 4;
   static constexpr int STAGES = (kSmemMax - kRest) / kStage > 10 ? 10 : (kSmemMax - kRest) / kStage;
-  static constexpr int kAccCols = BN < 32 ? 32 : BN;  // columns between the accumulators
-  static constexpr int kTmemCols = 2 * kAccCols;
+  static constexpr int kTmemCols = 2 * BN;  // two accumulators
   static constexpr uint32_t kIdesc = ptx::make_idesc(BM * CG, BN, Op::kFmt, Op::kFmt) |
                                      (Op::kAMn ? ptx::kIdescAMn : 0u) |
                                      (Op::kBMn ? ptx::kIdescBMn : 0u);
@@ -103,22 +101,14 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* tm
     if constexpr (CG == 2) ptx::tma_load_3d_pair(dst, tm, 0, k, mn / 64, bar);
     else ptx::tma_load_3d(dst, tm, 0, k, mn / 64, bar);
   } else {
-    constexpr int BOX = ROWS < 128 ? ROWS : 128;
-#pragma unroll
-    for (int g = 0; g < ROWS / BOX; ++g) {
-      if constexpr (CG == 2) ptx::tma_load_2d_pair(dst + g * BOX * 128, tm, k, mn + BOX * g, bar);
-      else ptx::tma_load_2d(dst + g * BOX * 128, tm, k, mn + BOX * g, bar);
-    }
+    static_assert(ROWS == 128, "one box of rows");
+    if constexpr (CG == 2) ptx::tma_load_2d_pair(dst, tm, k, mn, bar);
+    else ptx::tma_load_2d(dst, tm, k, mn, bar);
   }
 }
 
-// 32 accumulator columns of this thread's row, or zeros for an empty sum.
-__device__ __forceinline__ void load_acc32(uint32_t taddr, bool empty, float (&v)[32]) {
-  if (empty) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    return;
-  }
+// 32 accumulator columns of this thread's row.
+__device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
   __syncwarp();  // the load is one instruction of the whole warp
   ptx::tmem_ld32(taddr, r);
@@ -347,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t d = tmem_base + acc * C::kAccCols;
+          const uint32_t d = tmem_base + acc * C::BN;
           uint32_t more = 0;
           for (int n = Op::kChunk ? min(left, Op::kChunk) : left; n > 0; --n, --left) {
             if (!ptx::mbar_wait(full0 + at.bar, at.parity, status, kSiteMmaFull)) {
@@ -421,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto take = [&]() {
       ok = ptx::mbar_wait(accf0 + acc * 8, acc_ph, status, kSiteEpiAccFull);
       ptx::tc_fence_after();
-      return tmem_base + ((uint32_t)(q * 32) << 16) + acc * C::kAccCols;
+      return tmem_base + ((uint32_t)(q * 32) << 16) + acc * C::BN;
     };
     auto release = [&]() {
       ptx::tc_fence_before();
@@ -528,13 +518,13 @@ __device__ __forceinline__ void tile_starts(int E, int32_t* tile_start, F tiles)
 // ------------------------------------------------------------------ host
 // A row-major [rows, cols] matrix of 16-bit elements (cols contiguous) as an
 // operand of which a CTA holds `mn_rows` MN rows a stage: K-major (k = cols) in
-// boxes of 64 k by up to 128 rows, or MN-major (mn = cols, a multiple of 64) as
+// boxes of 64 k by mn_rows rows, or MN-major (mn = cols, a multiple of 64) as
 // cols / 64 groups, in boxes of 64 mn by 64 k rows by mn_rows / 64 groups. Rows
 // and columns past the matrix read as zeros.
 inline bool make_operand(CUtensorMap* m, const void* base, bool bf16, int64_t rows, int64_t cols, bool mn_major,
                          int mn_rows) {
   const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!mn_major) return make_tmap(m, base, dt, 2, cols, rows, std::min(mn_rows, 128));
+  if (!mn_major) return make_tmap(m, base, dt, 2, cols, rows, mn_rows);
   PFN_encodeTiled enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
@@ -545,9 +535,9 @@ inline bool make_operand(CUtensorMap* m, const void* base, bool bf16, int64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A row-major [items, rows, cols] tensor for an
-// epilogue warp's boxes: 32 rows by row_bytes (64 or 128) of one item. Copies
-// read zeros and write nothing past an item's rows and columns.
+// A row-major [items, rows, cols] tensor for an epilogue warp's boxes: 32 rows by
+// row_bytes (64 or 128) of one item. Copies read zeros and write nothing past an
+// item's rows and columns.
 inline bool make_boxes(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, int64_t items,
                        int64_t rows, int64_t cols, int row_bytes) {
   PFN_encodeTiled enc = get_encode();

@@ -139,7 +139,7 @@ struct Square {
       const int col = col0 + 32 * i;
       float v[32];
       if (POLY && i + 1 < n) load_gram(t, w, i + 1);  // its box's values were used two columns of boxes ago
-      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
+      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, v);
       if constexpr (POLY) {
         if (!w.wait(i & 1)) return false;
 #pragma unroll
@@ -271,7 +271,7 @@ struct Apply {
       w.free_boxes();
       if (i + 1 < n) load_state(t, w, i + 1);
       float v[32], x[32];
-      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, false, v);
+      load_acc32(taddr + w.half * (kBN / 2) + 32 * i, v);
       if (!w.wait(i & 1)) return false;
       if (st.from_g) {
         const float f = st.s * inv.y;

@@ -652,6 +652,53 @@ def test_training_step_is_repeatable_and_captures():
     assert not torch.equal(replayed["dx"], first["dx"])
 
 
+@pytest.mark.parametrize("ahead", ["nothing", "memset", "copy", "join"])
+def test_captured_alone_and_behind_other_nodes(ahead):
+    """Launches that may start early, as a graph's first node and behind nodes that are no kernels."""
+    R, N, K = 2600, 128, 256
+    gen = _gen(31)
+    G, M = _randn(gen, 2, 300, 200, dtype=torch.float32), _randn(gen, 2, 5, 90, dtype=torch.float32)
+    dC, A, B = _randn(gen, R, N), _randn(gen, R, K), _randn(gen, 1, N, K)
+    src, off = G.clone(), _offsets([R])
+    O, O2 = torch.empty(2, 300, 200, dtype=BF16, device="cuda"), torch.empty(2, 5, 90, dtype=BF16, device="cuda")
+    dB, dA = torch.empty(1, N, K, device="cuda"), torch.empty(R, K, dtype=BF16, device="cuda")
+    wss = [_ws(1 << 23), _ws(moe.moe_orthogonalize_workspace_size(2, 300, 200)),
+           _ws(moe.moe_orthogonalize_workspace_size(2, 5, 90))]
+
+    def work():
+        moe.moe_orthogonalize(G, 2, 300, 200, moe.MOE_GRAD_F32, 5, COEFFS, 1e-7, 1.0, O, wss[1])
+        moe.moe_orthogonalize(M, 2, 5, 90, moe.MOE_GRAD_F32, 5, COEFFS, 1e-7, 1.0, O2, wss[2])
+        moe.moe_grouped_gemm_wgrad(dC, A, off, R, 1, N, K, moe.MOE_GRAD_F32, 0, dB, ws=wss[0])
+        moe.moe_grouped_gemm_dgrad(dC, B, off, R, 1, N, K, 0, dA, ws=wss[0])
+
+    work()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (O, O2, dB, dA)]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if ahead == "memset":
+            moe.moe_clear_device_status(wss[1])
+        elif ahead == "copy":
+            G.copy_(src)
+        elif ahead == "join":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                G.copy_(src)
+            dC.mul_(1.0)
+            torch.cuda.current_stream().wait_stream(side)
+        work()
+    for _ in range(3):
+        for t in (O, O2, dB, dA):
+            t.fill_(7)
+        if ahead in ("copy", "join"):
+            G.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, w in zip((O, O2, dB, dA), want):
+            assert torch.equal(t, w)
+
+
 def test_two_streams_with_a_workspace_each():
     counts = [100, 3, 0, 261]
     E, R, N, K = len(counts), sum(counts), 384, 512
