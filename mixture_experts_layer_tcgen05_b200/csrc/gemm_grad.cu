@@ -63,14 +63,21 @@ __device__ __forceinline__ void load_row32(const __nv_bfloat16* src, float (&v)[
 // dg = d u a'(g), du = d a(g) and, with h given, a(g) u.
 enum RowSet { kAllRows, kPairRows, kRestRows };
 
-template <int ACT, bool PAIR>
+template <int ACT, bool PAIR, bool BOXED>
 struct RowGrad {
+  static_assert(BOXED || !PAIR, "a pair has the room");
   static constexpr bool kAMn = false, kBMn = true, kTail = false;
   static constexpr int kBN = 256, kFmt = 1, kChunk = 0;
-  // A pair stages boxes of 32 x 32: the result; gated, two of g and u each, which
-  // their gradients replace, and one of h. A single SM's wider stages leave no
-  // room for that beside enough of them, and its rows rarely fill a box.
-  static constexpr int kStageWarp = !PAIR ? 0 : ACT == kActNone ? 2048 : 10 * 1024;
+  // BOXED: boxes of 32 x 32 are staged: the result; gated, g and u, which their
+  // gradients replace, and h. A pair has room for g and u twice, the next ones on
+  // their way; beside a single SM's wider stages there is room for one, and for
+  // three stages instead of four. Not BOXED, lanes read and write rows of their
+  // own, which touches 32 lines at once and takes as long as the products of about
+  // 40 k blocks; so a single SM stages gated tiles where the sum is shorter (64
+  // experts' 16384 rows, N = 2048, K = 7168: 822 us in boxes, 1249 without; 256
+  // rows, N = K = 4096, bound by the weights: 353 and 327).
+  static constexpr int kGu = ACT == kActNone || !BOXED ? 0 : PAIR ? 2 : 1;  // boxes of g and u
+  static constexpr int kStageWarp = BOXED ? 2048 + kGu * 4096 : 0;
   static constexpr int kSharedInts = 2 * (gg::kMaxE + 1);
   static constexpr int kRows = PAIR ? 2 * BM : BM;
 
@@ -128,17 +135,17 @@ struct RowGrad {
     return max(0, min(kBN / 2, K - t.b_mn - w.half * (kBN / 2))) / 32;
   }
   __device__ __forceinline__ void load_gu(const Tile& t, Warp& w, int i) const {
-    const int col = t.b_mn + w.half * (kBN / 2) + 32 * i, row0 = w.row0(t.a_mn);
-    const uint32_t box = w.base + (i & 1) * 4096;
+    const int col = t.b_mn + w.half * (kBN / 2) + 32 * i, row0 = w.row0(t.a_mn), slot = kGu == 2 ? i & 1 : 0;
+    const uint32_t box = w.base + 2048 + slot * 4096, bar = w.bar + 8 * slot;
     if (w.lane == 0) {
-      ptx::mbar_arrive_expect_tx(w.bar + 8 * (i & 1), 4096);
-      ptx::tma_load_3d(box, &w.maps->c[1], col, row0, 0, w.bar + 8 * (i & 1));
-      ptx::tma_load_3d(box + 2048, &w.maps->c[1], K + col, row0, 0, w.bar + 8 * (i & 1));
+      ptx::mbar_arrive_expect_tx(bar, 4096);
+      ptx::tma_load_3d(box, &w.maps->c[1], col, row0, 0, bar);
+      ptx::tma_load_3d(box + 2048, &w.maps->c[1], K + col, row0, 0, bar);
     }
-    w.pending |= 1u << (i & 1);
+    w.pending |= 1u << slot;
   }
   __device__ void prefetch(const Tile& t, Warp& w) const {
-    if constexpr (PAIR && ACT != kActNone) {
+    if constexpr (kGu != 0) {
       if (steps(t, w) == 0) return;
       w.free_boxes();
       load_gu(t, w, 0);
@@ -166,39 +173,42 @@ struct RowGrad {
     const bool valid = row < t.p[0];
     // a box reaches past the expert's rows: what is past them is not this
     // expert's to write, so each lane stores its own row
-    const bool boxed = PAIR && row0 + 32 <= t.p[0];
+    const bool boxed = BOXED && row0 + 32 <= t.p[0];
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int c = w.half * (kBN / 2) + 32 * i, col = t.b_mn + c;
-      const uint32_t box = w.base + (i & 1) * 4096;
-      if constexpr (PAIR) {
-        w.free_boxes();
-        if (ACT != kActNone && i + 1 < n) load_gu(t, w, i + 1);
-      }
       float d[32];
-      load_acc32(taddr + c, d);
       if constexpr (ACT == kActNone) {
-        if (boxed) {
+        load_acc32(taddr + c, d);
+        if (kParts && part) {
+          if (valid) {
+            float4* dst = reinterpret_cast<float4*>(part + ((int64_t)t.p[1] * M_total + row) * K + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+          }
+        } else if (boxed) {
+          w.free_boxes();
           put_row(w.base, w.lane, d);
           w.publish();
           if (w.lane == 0) {
             ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, 0);
             ptx::bulk_commit();
           }
-        } else if (kParts && part) {
-          if (valid) {
-            float4* dst = reinterpret_cast<float4*>(part + ((int64_t)t.p[1] * M_total + row) * K + col);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
-          }
         } else if (valid) {
           gg::store_row32(dA + (int64_t)row * K + col, d);
         }
       } else {
+        const int slot = kGu == 2 ? i & 1 : 0;
         const int64_t at = (int64_t)row * 2 * K + col;
+        const uint32_t box = w.base + 2048 + slot * 4096;
+        if constexpr (BOXED) {
+          w.free_boxes();
+          if (kGu == 2 ? i + 1 < n : i > 0) load_gu(t, w, kGu == 2 ? i + 1 : i);
+        }
+        load_acc32(taddr + c, d);
         float g[32], u[32];
-        if constexpr (PAIR) {
-          if (!w.wait(i & 1)) return false;
+        if constexpr (BOXED) {
+          if (!w.wait(slot)) return false;
           get_row(box, w.lane, g);
           get_row(box + 2048, w.lane, u);
         } else if (valid) {
@@ -216,12 +226,12 @@ struct RowGrad {
         if (boxed) {
           put_row(box, w.lane, g);
           put_row(box + 2048, w.lane, d);
-          if (h) put_row(w.base + 8192, w.lane, u);
+          if (h) put_row(w.base, w.lane, u);
           w.publish();
           if (w.lane == 0) {
             ptx::tma_store_3d(&w.maps->c[0], box, col, row0, 0);
             ptx::tma_store_3d(&w.maps->c[0], box + 2048, K + col, row0, 0);
-            if (h) ptx::tma_store_3d(&w.maps->c[2], w.base + 8192, col, row0, 0);
+            if (h) ptx::tma_store_3d(&w.maps->c[2], w.base, col, row0, 0);
             ptx::bulk_commit();
           }
         } else if (valid) {
@@ -404,20 +414,28 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
                                  cudaStream_t s, const char** why) {
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int64_t out_cols = act == kActNone ? K : 2 * (int64_t)K;
-  // no expert fills more than half a pair's tile: one launch over all rows
+  // Pairs where they pay for their second launch, of the experts' last rows: 256
+  // rows an expert over many waves of tiles, or 1024 over a few. (us, pairs and
+  // singles: 16384 rows of 4 experts, N = K = 4096, 408 and 423; of 64, N = 2048,
+  // K = 7168, 588 and 624; 8192 rows of 16, N = 7168, K = 2048, 4 waves, 241 and
+  // 208; 4096 of 4, N = K = 4096, 125 and 112; 4096 of 64, 401 and 349.)
   const int most = max_rows_per_expert > 0 ? std::min(max_rows_per_expert, M_total) : M_total;
+  const int64_t each = M_total / E, all = ((int64_t)M_total / mm::BM + E / 2) * ceil_div(K, 256);
+  const bool many = most > mm::BM && each >= 256 &&
+                    (all >= 16 * (int64_t)num_sms() || (each >= 1024 && M_total >= 8192 && all >= 4 * (int64_t)num_sms()));
   const int64_t tiles_ub = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * ceil_div(K, 256);
   const int parts = mm::sum_parts(num_sms(), tiles_ub, N / mm::BK, (int64_t)M_total * K * 4, scratch_bytes);
-  const bool pairs = most > mm::BM && parts == 1;
-  mm::Maps pair = {}, single = {};
+  const bool pairs = many && parts == 1;
+  // (in parts, the tiles' results go to the scratch, by plain stores)
+  mm::Maps single = {}, pair = {};
   bool ok = mm::make_operand(&single.a, dC, true, M_total, N, false, mm::BM) &&
-            mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256);
+            mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256) &&
+            mm::make_boxes(&single.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) &&
+            (!gu || mm::make_boxes(&single.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) &&
+            (!h || mm::make_boxes(&single.c[2], h, bf16, 2, 1, M_total, K, 64));
   if (pairs) {
-    pair.a = single.a;
-    ok = ok && mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128) &&
-         mm::make_boxes(&pair.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) &&
-         (!gu || mm::make_boxes(&pair.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) &&
-         (!h || mm::make_boxes(&pair.c[2], h, bf16, 2, 1, M_total, K, 64));
+    pair = single;
+    ok = ok && mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128);
   }
   if (!ok) {
     *why = "cuTensorMapEncodeTiled failed";
@@ -446,16 +464,20 @@ cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* o
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
     if (parts > 1) {
-      cudaError_t e = go(mm::RowGrad<kActNone, false>{}, One{}, mm::kAllRows);
+      cudaError_t e = go(mm::RowGrad<kActNone, false, true>{}, One{}, mm::kAllRows);
       if (e != cudaSuccess) return e;
       const dim3 grid((unsigned)ceil_div(M_total, 8), (unsigned)ceil_div(K, 1024));
       return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, 1, static_cast<const float*>(scratch), parts,
                                    offsets, E, M_total, K, static_cast<const __nv_bfloat16*>(gu),
                                    static_cast<__nv_bfloat16*>(dA), static_cast<__nv_bfloat16*>(h));
     }
-    if (!pairs) return go(mm::RowGrad<ACT, false>{}, One{}, mm::kAllRows);
-    cudaError_t e = go(mm::RowGrad<ACT, true>{}, Two{}, mm::kPairRows);
-    return e != cudaSuccess ? e : go(mm::RowGrad<ACT, false>{}, One{}, mm::kRestRows);
+    if (pairs) {
+      cudaError_t e = go(mm::RowGrad<ACT, true, true>{}, Two{}, mm::kPairRows);
+      if (e != cudaSuccess) return e;
+    }
+    const mm::RowSet rows = pairs ? mm::kRestRows : mm::kAllRows;
+    return ACT == kActNone || N < 4096 ? go(mm::RowGrad<ACT, false, true>{}, One{}, rows)
+                                       : go(mm::RowGrad<ACT, false, ACT == kActNone>{}, One{}, rows);
   };
   switch (act) {
     case kActSilu: return both(std::integral_constant<int, kActSilu>{});
