@@ -308,15 +308,6 @@ struct Apply {
       }
       if (st.last) {
         const float r = st.scale * st.inv_s;
-        if (!st.vec) {  // rows of the result that a tiled store cannot address
-          if (row < st.rows) {
-            __nv_bfloat16* dst = st.out + ((int64_t)t.p[0] * st.rows + row) * st.cols + col;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j < st.cols) dst[j] = __float2bfloat16_rn(r * v[j]);
-          }
-          continue;
-        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t o[4];
@@ -333,6 +324,22 @@ struct Apply {
           Warp::put(Warp::at64(box, w.lane, u), make_uint4(o[0], o[1], o[2], o[3]));
           Warp::put(Warp::at64(box + 2048, w.lane, u), make_uint4(l[0], l[1], l[2], l[3]));
         }
+      }
+      if (st.last && !st.vec) {  // rows that a tiled store cannot address: row by row, lane = column
+        __syncwarp();
+        const int rows = min(32, st.rows - row0);
+        __nv_bfloat16* dst = st.out + ((int64_t)t.p[0] * st.rows + row0) * st.cols + col + w.lane;
+        if (col + w.lane < st.cols)
+          for (int r = 0; r < rows; ++r) {
+            unsigned short x;
+            asm volatile("ld.shared.b16 %0, [%1];"
+                         : "=h"(x)
+                         : "r"(Warp::at64(box, r, w.lane >> 3) + (w.lane & 7) * 2)
+                         : "memory");
+            dst[(int64_t)r * st.cols] = __ushort_as_bfloat16(x);
+          }
+        __syncwarp();
+        continue;
       }
       w.publish();
       if (w.lane == 0) {
@@ -406,31 +413,46 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const
   const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
   const float p = (float)p2, r = (float)(1.0 / (norm * p2 + (double)eps * p2));
   if (blockIdx.x == 0 && threadIdx.x == 0) inv[b] = make_float2(p, r);
-  const int vpr = st.np / 8;
-  const int64_t vecs = (int64_t)st.mp * vpr;
   const T* src = static_cast<const T*>(st.g) + b * st.rows * st.cols;
   const int64_t base = b * st.mp * st.np;
+  // odd rows: a warp takes 64 columns of a row at a time, lane = column (with the
+  // result's stores likewise: 51 of 198 x 3553, one step, 241 us; eight columns a
+  // lane and rows stored by their own lanes 560)
+  if (!st.vec) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = st.np / 64;
+    for (int64_t u = (int64_t)blockIdx.x * (kNormThreads / 32) + warp; u < (int64_t)st.mp * blocks;
+         u += (int64_t)gridDim.x * (kNormThreads / 32)) {
+      const int row = (int)(u / blocks), col = (int)(u % blocks) * 64 + lane;
+      float x[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        x[j] = row < st.rows && col + 32 * j < st.cols ? p * (float)src[(int64_t)row * st.cols + col + 32 * j] * r * st.s
+                                                        : 0.0f;
+      uint32_t hi, lo;
+      split(x[0], x[1], hi, lo);
+      const int64_t at = base + (int64_t)row * st.np + col;
+      xh[at] = __ushort_as_half((unsigned short)hi), xh[at + 32] = __ushort_as_half((unsigned short)(hi >> 16));
+      if (xl) xl[at] = __ushort_as_half((unsigned short)lo), xl[at + 32] = __ushort_as_half((unsigned short)(lo >> 16));
+    }
+    return;
+  }
+  const int vpr = st.np / 8;
+  const int64_t vecs = (int64_t)st.mp * vpr;
   for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < vecs;
        i += (int64_t)gridDim.x * kNormThreads) {
     const int row = (int)(i / vpr), col = (int)(i % vpr) * 8;
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-    if (row < st.rows) {
+    if (row < st.rows && col < st.cols) {  // cols is a multiple of 8: all eight or none
       const T* at = src + (int64_t)row * st.cols + col;
-      if (st.vec && col + 8 <= st.cols) {
-        if constexpr (sizeof(T) == 4) {
-          const float4 lo = __ldg(reinterpret_cast<const float4*>(at)), hi = __ldg(reinterpret_cast<const float4*>(at) + 1);
-          x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-        } else {
-          const uint4 o = __ldg(reinterpret_cast<const uint4*>(at));
-          x[0] = bf16lo_to_f32(o.x), x[1] = bf16hi_to_f32(o.x), x[2] = bf16lo_to_f32(o.y), x[3] = bf16hi_to_f32(o.y);
-          x[4] = bf16lo_to_f32(o.z), x[5] = bf16hi_to_f32(o.z), x[6] = bf16lo_to_f32(o.w), x[7] = bf16hi_to_f32(o.w);
-        }
+      if constexpr (sizeof(T) == 4) {
+        const float4 lo = __ldg(reinterpret_cast<const float4*>(at)), hi = __ldg(reinterpret_cast<const float4*>(at) + 1);
+        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < st.cols) x[j] = (float)at[j];
+        const uint4 o = __ldg(reinterpret_cast<const uint4*>(at));
+        x[0] = bf16lo_to_f32(o.x), x[1] = bf16hi_to_f32(o.x), x[2] = bf16lo_to_f32(o.y), x[3] = bf16hi_to_f32(o.y);
+        x[4] = bf16lo_to_f32(o.z), x[5] = bf16hi_to_f32(o.z), x[6] = bf16lo_to_f32(o.w), x[7] = bf16hi_to_f32(o.w);
       }
     }
     uint32_t o[4], l[4];
