@@ -263,9 +263,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) ptx::cluster_sync();  // both CTAs' barriers exist before anyone signals them
   ptx::tc_fence_after();
   ptx::let_next_grid_start();
-  ptx::wait_for_previous_grid();
+  // Without tables to fill, the first tile's place needs nothing of the grid
+  // ahead: found before the wait, it also brings the parameters into the caches.
+  constexpr bool kEarly = Op::kSharedInts == 0;
   const uint32_t tmem_base = *tmem_slot;
-  const int total = op.total(sh);
+  Tile t;  // each role's own, from here on
+  int total;
+  if constexpr (kEarly) {
+    total = op.total(sh);
+    if (unit0 < total) op.decode(sh, unit0, t);
+  }
+  ptx::wait_for_previous_grid();
+  if constexpr (!kEarly) {
+    total = op.total(sh);
+    if (unit0 < total) op.decode(sh, unit0, t);
+  }
+  // the next tile of a role's loop
+  auto next = [&](int tile) {
+    tile += units;
+    if (tile < total) op.decode(sh, tile, t);
+    return tile;
+  };
   // The producer's and the MMA issuer's loops run in one thread each, so a k
   // block costs them their instructions' latencies: positions in the ring are
   // stepped, not divided out (measured: a loop with 64-bit quotients took 675
@@ -274,9 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring<STAGES, C::kStage> at(sbase);
       bool ok = true;
-      for (int tile = unit0; tile < total && ok; tile += units) {
-        Tile t;
-        op.decode(sh, tile, t);
+      for (int tile = unit0; tile < total && ok; tile = next(tile)) {
         const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
         int ka = t.a_k, kbb = t.b_k;
         for (int left = t.nkb; left > 0; --left, ka += BK, kbb += BK) {
@@ -327,9 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (CG == 2) ptx::mma_commit_pair(bar);
         else ptx::mma_commit(bar);
       };
-      for (int tile = unit0; tile < total && ok; tile += units) {
-        Tile t;
-        op.decode(sh, tile, t);
+      for (int tile = unit0; tile < total && ok; tile = next(tile)) {
         int left = t.nkb;
         do {  // once without chunks; an empty sum still hands over its (unread) accumulator
           if (!ptx::mbar_wait(acce0 + acc * 8, acc_ph ^ 1, status, kSiteMmaAccEmpty)) {
@@ -373,9 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (Op::kTail) {
       int slot = 0;         // stage of the tile's first k block
       uint32_t phases = 0;  // bit s: parity of tail[s]'s next phase
-      for (int tile = unit0; tile < total; tile += units) {
-        Tile t;
-        op.decode(sh, tile, t);
+      for (int tile = unit0; tile < total; tile = next(tile)) {
         const int s = (slot + t.nkb + STAGES - 1) % STAGES;  // of its last one
         slot = (slot + t.nkb) % STAGES;
         if (t.nkb == 0 || !(t.tail & (UK - 1))) continue;
@@ -423,9 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_ph ^= 1;
     };
-    for (int tile = unit0; tile < total && ok; tile += units) {
-      Tile t;
-      op.decode(sh, tile, t);
+    for (int tile = unit0; tile < total && ok; tile = next(tile)) {
       if constexpr (Op::kChunk != 0) {
         // The first (often the only) partial sum is read straight into place,
         // all its loads in flight at once; later ones are added 16 columns at a time.
