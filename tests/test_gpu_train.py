@@ -87,6 +87,8 @@ GROUPS = [
     ([640, 2, 0, 500], 1152, 896),
     ([1] * 40, 128, 256),
     ([2100], 256, 256),
+    ([1, 0, 2, 0] * 256, 128, 128),  # 1024 experts
+    ([1100, 1300, 0, 1500, 700, 1, 1900, 1692], 1024, 4992),  # pairs of SMs and their last rows
 ]
 
 
