@@ -150,16 +150,30 @@ def _p(a):
     raise TypeError(f"cannot take the address of {type(a)}")
 
 
+_cuda = None  # (current device, its current stream's handle), as functions
+
+
+def _cuda_calls():
+    """torch's calls without their wrappers, which build a Stream object and initialise lazily (3 us a call)."""
+    global _cuda
+    if _cuda is None:
+        import torch
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.current_device()  # (initialises)
+        _cuda = device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _cuda
+
+
 def _ts(*args):
     """Addresses of dense tensors on the current device / ints / None: what a kernel there may read or write."""
     current, out = None, []
     for a in args:
-        if a is not None and not isinstance(a, int):
+        if a is not None and a.__class__ is not int:
             device = a.get_device()
             if current is None and device >= 0:
-                import torch
-                current = torch.cuda.current_device()
-            if device < 0 or device != current:
+                current = _cuda_calls()[0]()
+            if device != current or device < 0:
                 raise MoeError(MOE_ERR_INVALID_ARG, f"a tensor is on {a.device}, not on the current CUDA device")
             if not a.is_contiguous():
                 raise MoeError(MOE_ERR_INVALID_ARG, f"a tensor of shape {tuple(a.shape)} has strides {a.stride()}: "
@@ -171,12 +185,8 @@ def _ts(*args):
 
 def _s(stream):
     if stream is None:
-        import torch
-        # (torch.cuda.current_stream() builds a Stream object around the same handle: 3 us a call)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        device, raw = _cuda_calls()
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
