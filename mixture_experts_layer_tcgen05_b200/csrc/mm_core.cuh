@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5 + 2 * kEpiWarps);
   int32_t* sh = reinterpret_cast<int32_t*>(stage_out + C::kStageOut + kBarBytes);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the same in every lane, and known to be: the roles' loops keep their state in
+  // uniform registers, where the MMA takes its operands from)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)ptx::cluster_ctarank() : 0;
   const int unit0 = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
   const uint32_t sbase = ptx::smem_addr(smem);
@@ -323,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      // The whole warp walks the tiles and waits, one lane issues.
+      const bool issuer = ptx::elect_one();
       Ring<STAGES, C::kStage> at(sbase);
       int acc = 0;
       uint32_t acc_ph = 0;
@@ -361,27 +365,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t off = (at.stage - sbase) >> 4;
             const uint64_t da = da0 + off, db = db0 + off;
-            if (Op::kTail && left == 1) {  // no 16-row step past the last row
-              for (int kk = 0; kk * UK < t.tail; ++kk, more = 1) mma(d, da + kk * stepA, db + kk * stepB, more);
-            } else {
-              mma(d, da, db, more);
+            if (issuer) {
+              if (Op::kTail && left == 1) {  // no 16-row step past the last row
+                for (int kk = 0; kk * UK < t.tail; ++kk) mma(d, da + kk * stepA, db + kk * stepB, kk ? 1 : more);
+              } else {
+                mma(d, da, db, more);
 #pragma unroll
-              for (int kk = 1; kk < BK / UK; ++kk) mma(d, da + kk * stepA, db + kk * stepB, 1);
+                for (int kk = 1; kk < BK / UK; ++kk) mma(d, da + kk * stepA, db + kk * stepB, 1);
+              }
+              commit(empty0 + at.bar);
             }
             more = 1;
-            commit(empty0 + at.bar);
             at.step();
           }
           if (!ok) break;
-          commit(accf0 + acc * 8);
+          if (issuer) commit(accf0 + acc * 8);
           acc ^= 1;
           if (acc == 0) acc_ph ^= 1;
         } while (left > 0);
       }
-      // every MMA this thread issued has completed once `drain` fires
-      if constexpr (CG == 2) ptx::mma_commit_pair(drain);
-      else ptx::mma_commit(drain);
-      ptx::mbar_wait(drain, 0, status, kSiteDrain);
+      // every MMA that was issued has completed once `drain` fires
+      if (issuer) {
+        commit(drain);
+        ptx::mbar_wait(drain, 0, status, kSiteDrain);
+      }
     }
   } else if (warp == 2) {
     if constexpr (Op::kTail) {
