@@ -286,22 +286,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tile < total) op.decode(sh, tile, t);
     return tile;
   };
-  // The producer's and the MMA issuer's loops run in one thread each, so a k
-  // block costs them their instructions' latencies: positions in the ring are
-  // stepped, not divided out (measured: a loop with 64-bit quotients took 675
-  // cycles a block, whatever the MMA's size; the MMAs themselves take 512).
+  // The producer's and the MMA issuer's loops run in one warp each, so a k block
+  // costs them their instructions' latencies: positions in the ring are stepped,
+  // not divided out (measured without loads: a loop with 64-bit quotients took 675
+  // cycles a block, whatever the MMA's size, and 593 without them; @N with the
+  // whole warp in the loop; the MMAs themselves take 512).
   if (warp == 0) {
-    if (lane == 0) {
-      Ring<STAGES, C::kStage> at(sbase);
-      bool ok = true;
-      for (int tile = unit0; tile < total && ok; tile = next(tile)) {
-        const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
-        int ka = t.a_k, kbb = t.b_k;
-        for (int left = t.nkb; left > 0; --left, ka += BK, kbb += BK) {
-          if (!ptx::mbar_wait(empty0 + at.bar, at.parity ^ 1, status, kSiteProducerEmpty)) {
-            ok = false;
-            break;
-          }
+    // The whole warp walks the tiles and waits, one lane loads.
+    const bool loader = ptx::elect_one();
+    Ring<STAGES, C::kStage> at(sbase);
+    bool ok = true;
+    for (int tile = unit0; tile < total && ok; tile = next(tile)) {
+      const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
+      int ka = t.a_k, kbb = t.b_k;
+      for (int left = t.nkb; left > 0; --left, ka += BK, kbb += BK) {
+        if (!ptx::mbar_wait(empty0 + at.bar, at.parity ^ 1, status, kSiteProducerEmpty)) {
+          ok = false;
+          break;
+        }
+        if (loader) {
           uint32_t bar;
           if (Op::kTail && left == 1 && (t.tail & (UK - 1))) {
             bar = tail0 + at.bar;  // this CTA's warp 2 waits for the bytes and arrives on `full` itself
@@ -313,15 +316,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           load_operand<Op::kAMn, BM, CG>(at.stage, &maps.a, am, ka, bar);
           load_operand<Op::kBMn, C::kBRows, CG>(at.stage + kTileA, &maps.b, bn, kbb, bar);
-          at.step();
         }
+        at.step();
       }
-      // every load of the ring has landed before this CTA (for a pair: both) goes
-      if (rank == 0) {
-        for (uint32_t b = 0; b < STAGES * 8; b += 8) {
-          const bool again = b < at.bar;  // used since the ring last began
-          if (again || at.wrapped) ptx::mbar_wait(full0 + b, again ? at.parity : at.parity ^ 1, status, kSiteDrain);
-        }
+    }
+    // every load of the ring has landed before this CTA (for a pair: both) goes
+    if (loader && rank == 0) {
+      for (uint32_t b = 0; b < STAGES * 8; b += 8) {
+        const bool again = b < at.bar;  // used since the ring last began
+        if (again || at.wrapped) ptx::mbar_wait(full0 + b, again ? at.parity : at.parity ^ 1, status, kSiteDrain);
       }
     }
   } else if (warp == 1) {
