@@ -397,8 +397,6 @@ typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
  *   gu_dev bf16 [M_total, 2K] (gated: g, then u, per row), else NULL
  *   dA_dev bf16 [M_total, K], gated [M_total, 2K]
  *   h_dev  bf16 [M_total, K] or NULL (gated), else NULL
- *   max_rows_per_expert: a bound on any expert's rows (0 = unknown); bounds <=
- *          128 save a launch. More rows than the bound are not an error.
  * N, K multiples of 128 up to 2^24, E*N < 2^31. Accumulation is fp32; every
  * output is rounded once. Offsets are clamped to [0, M_total]; rows of no expert
  * are left as they were. Outputs overlap neither inputs nor each other.
@@ -411,8 +409,7 @@ typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
 moe_status_t moe_grouped_gemm_dgrad(const void* dC_dev, const void* B_dev, const int32_t* offsets_dev,
                                     int32_t M_total, int32_t E, int32_t N, int32_t K,
                                     moe_epilogue_t ep, const void* gu_dev, void* dA_dev, void* h_dev,
-                                    int32_t max_rows_per_expert, void* ws, size_t ws_bytes,
-                                    void* stream);
+                                    void* ws, size_t ws_bytes, void* stream);
 
 /* Gradient of moe_grouped_gemm (bf16) with respect to the experts' weights:
  *   dB[e, n, k] (+)= sum over the rows m of expert e of dC[m, n] A[m, k]

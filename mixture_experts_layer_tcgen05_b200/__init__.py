@@ -105,7 +105,7 @@ _SIGS = {
     "moe_ep_dispatch": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp, _i64, _vp, _vp]),
     "moe_ep_return": (_i32, [_vp, _vp, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp]),
     "moe_grouped_gemm_dgrad": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
-                                      _i32, _vp, _sz, _vp]),
+                                      _vp, _sz, _vp]),
     "moe_grouped_gemm_wgrad": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
                                       _sz, _vp]),
     "moe_combine_backward": (_i32, [_vp, _vp, _vp, _vp, Dims, _vp, _vp, _vp, _vp]),
@@ -373,11 +373,11 @@ def moe_ep_return(y_loc, plan, E, G, cap_rows, row_bytes, src_bufs, src_rows, ws
                                src_rows, _p(ws), _s(stream)))
 
 
-def moe_grouped_gemm_dgrad(dC, B, offsets, M_total, E, N, K, ep, dA, gu=None, h=None,
-                           max_rows_per_expert=0, ws=None, ws_bytes=None, stream=None):
+def moe_grouped_gemm_dgrad(dC, B, offsets, M_total, E, N, K, ep, dA, gu=None, h=None, ws=None,
+                           ws_bytes=None, stream=None):
     pdC, pB, po, pgu, pdA, ph, pws = _ts(dC, B, offsets, gu, dA, h, ws)
     _check(lib().moe_grouped_gemm_dgrad(pdC, pB, po, M_total, E, N, K, ep, pgu, pdA, ph,
-                                        max_rows_per_expert, pws, _nbytes(ws, ws_bytes), _s(stream)))
+                                        pws, _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def moe_grouped_gemm_wgrad(dC, A, offsets, M_total, E, N, K, type, accumulate, dB, ws=None,

@@ -89,8 +89,8 @@ cudaError_t noalloc_status(int32_t* out, bool clear);
 // training (gemm_grad.cu, combine_grad.cu, orthogonalize.cu)
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int max_rows_per_expert, int32_t* status, void* scratch,
-                                 size_t scratch_bytes, cudaStream_t s, const char** why);
+                                 int32_t* status, void* scratch, size_t scratch_bytes, cudaStream_t s,
+                                 const char** why);
 cudaError_t launch_grouped_wgrad(const void* dC, const void* A, const int32_t* offsets, int M_total,
                                  int E, int N, int K, bool f32, bool add, void* dB, int32_t* status,
                                  void* scratch, size_t scratch_bytes, cudaStream_t s, const char** why);
@@ -501,12 +501,9 @@ moe_status_t check_grad_dims(int32_t M_total, int32_t E, int32_t N, int32_t K) {
 
 moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t* offsets, int32_t M_total,
                                     int32_t E, int32_t N, int32_t K, moe_epilogue_t ep, const void* gu,
-                                    void* dA, void* h, int32_t max_rows_per_expert, void* ws,
-                                    size_t ws_bytes, void* stream) {
+                                    void* dA, void* h, void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(check_grad_dims(M_total, E, N, K));
   if (ep < MOE_EPILOGUE_NONE || ep > MOE_EPILOGUE_REGLU) return fail(MOE_ERR_INVALID_ARG, "bad epilogue");
-  if (max_rows_per_expert < 0)
-    return fail(MOE_ERR_INVALID_ARG, "max_rows_per_expert must be >= 0 (got %d)", max_rows_per_expert);
   MOE_TRY(check_ptr(dC, "dC"));
   MOE_TRY(check_ptr(B, "B"));
   MOE_TRY(check_ptr(offsets, "expert_offsets"));
@@ -533,7 +530,7 @@ moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, const int32_t
   if (overlaps(dA, out, h, M * K * 2)) return fail(MOE_ERR_INVALID_ARG, "dA and h overlap");
   MOE_TRY(check_device());
   const char* why = "";
-  cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h, max_rows_per_expert,
+  cudaError_t e = launch_grouped_dgrad(dC, B, offsets, M_total, E, N, K, (int)ep, gu, dA, h,
                                        at<int32_t>(ws, 0), at<char>(ws, 256), scratch ? ws_bytes - 256 : 0,
                                        static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped GEMM row gradient: %s %s", cudaGetErrorString(e), why);

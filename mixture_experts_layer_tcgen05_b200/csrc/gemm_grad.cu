@@ -35,81 +35,56 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& da) {
   }
 }
 
-__device__ __forceinline__ void load_row32(const __nv_bfloat16* src, float (&v)[32]) {
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 x = __ldg(s + q);
-    v[8 * q + 0] = bf16lo_to_f32(x.x);
-    v[8 * q + 1] = bf16hi_to_f32(x.x);
-    v[8 * q + 2] = bf16lo_to_f32(x.y);
-    v[8 * q + 3] = bf16hi_to_f32(x.y);
-    v[8 * q + 4] = bf16lo_to_f32(x.z);
-    v[8 * q + 5] = bf16hi_to_f32(x.z);
-    v[8 * q + 6] = bf16lo_to_f32(x.w);
-    v[8 * q + 7] = bf16hi_to_f32(x.w);
-  }
-}
-
-// Tiles of one expert's rows by 256 columns, in the order of the forward's
-// 128-row GEMM: expert, band of m-tiles, n-tile, m-tile. PAIR: 256 rows of a
-// pair of SMs, else 128. A k block of a 128-row tile brings 48 KB for 512 cycles
-// of MMA (the pair's 32 KB per SM), which at full rate is more than L2 delivers;
-// but an expert's last 128 rows or fewer would leave half a pair's tile empty.
-// So an expert's rows go to pairs as far as they fill more than half a tile, and
-// a remainder of at most 128 rows to single SMs, in a second launch that starts
-// as the first one's SMs run out of tiles.
+// The product with the weights' columns (k, along memory) as the MMA's M and the
+// expert's rows as its N, whose size is free: an expert with c rows takes
+// ceil(c / kBN) tiles of as many rows each, rounded up to 16. The MMA's time goes
+// with N (558 cycles a k block at N = 256, 418 at 192, 345 at 128 and below, where
+// issuing it takes longest), so rows past an expert's end cost next to nothing.
+// With the rows in M, tiles of 128 made the fine-grained case's MMAs a fifth
+// longer. Tiles are 256 columns by up to 256 rows of a pair of SMs, or, for K =
+// 128, 128 by up to 128 of one; by up to 64 rows of a pair where the call has at
+// most 32 rows per expert on average: reading the weights is all there is to it
+// then, and shorter tiles leave room for 8 to 10 stages of them instead of 4 to 6.
+// Gated, 64 experts of 4096 x 14336 with 1024 rows: 1116 us so, 1241 with tiles of
+// 256; with 4096 rows 1484 and 1400. Order: expert, band of row tiles, column tile, row
+// tile, so that pairs that run together share the weights' columns.
+// The accumulator's lanes are columns of the result and its columns rows: an
+// epilogue warp takes 32 x 32 of it at a time, writes it transposed to a box and
+// stores that where the expert has all 32 rows, else row by row. Gated, the fp32
+// product is turned first, half of it at a time, so that g, u and what becomes of
+// them are read and written 16 bytes a lane: 2 bytes a lane took 173 us for 1024 x
+// 1024 and 16384 rows of 64 experts, this 70.
 // ACT: the product is the gradient d of h = a(g) u; the epilogue writes
 // dg = d u a'(g), du = d a(g) and, with h given, a(g) u.
-enum RowSet { kAllRows, kPairRows, kRestRows };
-
-template <int ACT, bool PAIR, bool BOXED>
+template <int ACT, int CG, int BN>
 struct RowGrad {
-  static_assert(BOXED || !PAIR, "a pair has the room");
-  static constexpr bool kAMn = false, kBMn = true, kTail = false;
-  static constexpr int kBN = 256, kFmt = 1, kChunk = 0;
-  // BOXED: boxes of 32 x 32 are staged: the result; gated, g and u, which their
-  // gradients replace, and h. A pair has room for g and u twice, the next ones on
-  // their way; beside a single SM's wider stages there is room for one, and for
-  // three stages instead of four. Not BOXED, lanes read and write rows of their
-  // own, which touches 32 lines at once and takes as long as the products of about
-  // 40 k blocks; so a single SM stages gated tiles where the sum is shorter (64
-  // experts' 16384 rows, N = 2048, K = 7168: 822 us in boxes, 1249 without; 256
-  // rows, N = K = 4096, bound by the weights: 353 and 327).
-  static constexpr int kGu = ACT == kActNone || !BOXED ? 0 : PAIR ? 2 : 1;  // boxes of g and u
-  static constexpr int kStageWarp = BOXED ? 2048 + kGu * 4096 : 0;
+  static constexpr bool kAMn = true, kBMn = false, kTail = false, kVarN = true;
+  static constexpr int kBN = BN, kCols = BM * CG, kFmt = 1, kChunk = 0;
+  // Boxes of 32 x 32 are staged: the result; gated, the product while it is turned,
+  // whose place h takes, and two of g and u each (the next ones on their way; tiles
+  // of 64 rows have one only), which their gradients replace.
+  static constexpr int kStageWarp = ACT == kActNone ? 2048 : 2048 + 4096 * (BN > 64 ? 2 : 1);
   static constexpr int kSharedInts = 2 * (gg::kMaxE + 1);
-  static constexpr int kRows = PAIR ? 2 * BM : BM;
+  static constexpr int kBand = 8;
 
   const int32_t* offsets;
-  int E, M_total, N, K, NT, band;
-  RowSet set;
-  int parts;    // ranges of n that run as tiles of their own; above 1, single SMs only, and
-  float* part;  // their fp32 sums go here, [parts, M_total, K]
-  const __nv_bfloat16* gu;  // [M_total, 2K]
+  int E, M_total, N, K, NT;
+  int parts;    // ranges of n that run as tiles of their own; above 1,
+  float* part;  // their fp32 sums go here, [parts, M_total, K] (ACT none)
   __nv_bfloat16* dA;        // [M_total, K], with ACT [M_total, 2K]
   __nv_bfloat16* h;         // [M_total, K] or nullptr
-
-  // m-tiles of an expert with c rows, and its first row in them
-  __device__ __forceinline__ int m_tiles(int c) const {
-    if (PAIR) return c / 256 + (c % 256 > 128);
-    if (set == kRestRows) return c % 256 >= 1 && c % 256 <= 128;
-    return (c + BM - 1) / BM;
-  }
-  __device__ __forceinline__ int first_row(int c) const { return !PAIR && set == kRestRows ? c / 256 * 256 : 0; }
 
   __device__ void setup(int32_t* sh) const {
     int32_t* soff = sh + gg::kMaxE + 1;
     load_offsets(offsets, E, M_total, soff);
-    tile_starts(E, sh, [&](int e) { return m_tiles(max(soff[e + 1] - soff[e], 0)) * NT; });
+    tile_starts(E, sh, [&](int e) { return (max(soff[e + 1] - soff[e], 0) + kBN - 1) / kBN * NT; });
   }
-  static constexpr bool kParts = !PAIR && ACT == kActNone;
-  __device__ int total(const int32_t* sh) const { return sh[E] * (kParts ? parts : 1); }
+  __device__ int total(const int32_t* sh) const { return sh[E] * (ACT == kActNone ? parts : 1); }
   __device__ void decode(const int32_t* sh, int tile, Tile& t) const {
     const int32_t* soff = sh + gg::kMaxE + 1;
     t.nkb = N / BK;
     int kb0 = 0;
-    if constexpr (kParts) {
+    if constexpr (ACT == kActNone) {
       const int p = tile % parts, nkb = t.nkb;
       tile /= parts;
       kb0 = (int)((int64_t)nkb * p / parts);
@@ -118,103 +93,128 @@ struct RowGrad {
     }
     const int e = gg::find_expert(sh, E, tile);
     const int local = tile - sh[e], c = soff[e + 1] - soff[e];
-    const int bsz = band * NT;
+    const int mt = (c + kBN - 1) / kBN, each = ((c + mt - 1) / mt + 15) / 16 * 16;
+    const int bsz = kBand * NT;
     const int b = local / bsz;
-    const int rows = min(band, m_tiles(c) - b * band);
+    const int rows = min(kBand, mt - b * kBand);
     const int l2 = local - b * bsz;
-    const int n = l2 / rows, m = b * band + l2 % rows;
-    t.a_mn = soff[e] + first_row(c) + m * kRows;
-    t.a_k = kb0 * BK;
-    t.b_mn = n * kBN;
-    t.b_k = e * N + kb0 * BK;
+    const int n = l2 / rows, m = b * kBand + l2 % rows;
+    t.a_mn = n * kCols;
+    t.a_k = e * N + kb0 * BK;
+    t.b_mn = soff[e] + m * each;
+    t.b_k = kb0 * BK;
+    t.n = each;
     t.tail = BK;
-    t.p[0] = soff[e + 1];
+    t.p[0] = min(each, c - m * each);  // rows of the tile
   }
+  // this warp's 32 columns, and its share of the tile's groups of 32 rows: every other one
+  __device__ __forceinline__ int col0(const Tile& t, const Warp& w) const { return t.a_mn + w.rank * BM + w.q * 32; }
   __device__ __forceinline__ int steps(const Tile& t, const Warp& w) const {
-    if (w.row0(t.a_mn) >= t.p[0]) return 0;
-    return max(0, min(kBN / 2, K - t.b_mn - w.half * (kBN / 2))) / 32;
+    return col0(t, w) < K ? ((t.p[0] + 31) / 32 - w.half + 1) / 2 : 0;
   }
   __device__ __forceinline__ void load_gu(const Tile& t, Warp& w, int i) const {
-    const int col = t.b_mn + w.half * (kBN / 2) + 32 * i, row0 = w.row0(t.a_mn), slot = kGu == 2 ? i & 1 : 0;
-    const uint32_t box = w.base + 2048 + slot * 4096, bar = w.bar + 8 * slot;
+    const int row = t.b_mn + 32 * (2 * i + w.half), col = col0(t, w);
+    const uint32_t box = w.base + 2048 + (i & 1) * 4096, bar = w.bar + 8 * (i & 1);
     if (w.lane == 0) {
       ptx::mbar_arrive_expect_tx(bar, 4096);
-      ptx::tma_load_3d(box, &w.maps->c[1], col, row0, 0, bar);
-      ptx::tma_load_3d(box + 2048, &w.maps->c[1], K + col, row0, 0, bar);
+      ptx::tma_load_3d(box, &w.maps->c[1], col, row, 0, bar);
+      ptx::tma_load_3d(box + 2048, &w.maps->c[1], K + col, row, 0, bar);
     }
-    w.pending |= 1u << slot;
+    w.pending |= 1u << (i & 1);
   }
   __device__ void prefetch(const Tile& t, Warp& w) const {
-    if constexpr (kGu != 0) {
+    if constexpr (ACT != kActNone) {
       if (steps(t, w) == 0) return;
       w.free_boxes();
       load_gu(t, w, 0);
     }
   }
-  static __device__ __forceinline__ void put_row(uint32_t box, int lane, const float (&v)[32]) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      Warp::put(Warp::at64(box, lane, u),
-                make_uint4(pack_bf16x2(v[8 * u], v[8 * u + 1]), pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
-                           pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), pack_bf16x2(v[8 * u + 6], v[8 * u + 7])));
+  // element (row r, this lane's column) of a box
+  static __device__ __forceinline__ uint32_t at(uint32_t box, int r, int lane) {
+    return Warp::at64(box, r, lane >> 3) + (lane & 7) * 2;
   }
-  static __device__ __forceinline__ void get_row(uint32_t box, int lane, float (&v)[32]) {
+  static __device__ __forceinline__ void put(uint32_t addr, float v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+  }
+  // Gated, a lane holds columns 16 (lane & 1) .. + 15 of the rows lane / 2 and
+  // 16 + lane / 2 of 32 x 32: pieces of 8 columns, p of the first row and p - 2 of the
+  // second, which for eight lanes are spread over all banks.
+  static __device__ __forceinline__ uint32_t piece(uint32_t box, int lane, int p) {
+    return Warp::at64(box, lane / 2 + p / 2 * 16, (lane & 1) * 2 + p % 2);
+  }
+  static __device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+  static __device__ __forceinline__ void put_half(uint32_t box, int lane, const float (&v)[32]) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4 x = Warp::get(Warp::at64(box, lane, u));
-      v[8 * u] = bf16lo_to_f32(x.x), v[8 * u + 1] = bf16hi_to_f32(x.x);
-      v[8 * u + 2] = bf16lo_to_f32(x.y), v[8 * u + 3] = bf16hi_to_f32(x.y);
-      v[8 * u + 4] = bf16lo_to_f32(x.z), v[8 * u + 5] = bf16hi_to_f32(x.z);
-      v[8 * u + 6] = bf16lo_to_f32(x.w), v[8 * u + 7] = bf16hi_to_f32(x.w);
+    for (int p = 0; p < 4; ++p) Warp::put(piece(box, lane, p), pack8(v + 8 * p));
+  }
+  static __device__ __forceinline__ void get_half(uint32_t box, int lane, float (&v)[32]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint4 x = Warp::get(piece(box, lane, p));
+      v[8 * p] = bf16lo_to_f32(x.x), v[8 * p + 1] = bf16hi_to_f32(x.x);
+      v[8 * p + 2] = bf16lo_to_f32(x.y), v[8 * p + 3] = bf16hi_to_f32(x.y);
+      v[8 * p + 4] = bf16lo_to_f32(x.z), v[8 * p + 5] = bf16hi_to_f32(x.z);
+      v[8 * p + 6] = bf16lo_to_f32(x.w), v[8 * p + 7] = bf16hi_to_f32(x.w);
+    }
+  }
+  // v[r] of the lane's column becomes what the lane holds of its two rows
+  static __device__ __forceinline__ void turn(uint32_t box, int lane, float (&v)[32]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (p) __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(Warp::at128(box, r, lane >> 2) + (lane & 3) * 4), "f"(v[16 * p + r])
+                     : "memory");
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = Warp::get(Warp::at128(box, lane / 2, (lane & 1) * 4 + j));
+        v[16 * p + 4 * j] = __uint_as_float(x.x), v[16 * p + 4 * j + 1] = __uint_as_float(x.y);
+        v[16 * p + 4 * j + 2] = __uint_as_float(x.z), v[16 * p + 4 * j + 3] = __uint_as_float(x.w);
+      }
     }
   }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
-    const int row0 = w.row0(t.a_mn), row = row0 + w.lane, n = steps(t, w);
-    const bool valid = row < t.p[0];
-    // a box reaches past the expert's rows: what is past them is not this
-    // expert's to write, so each lane stores its own row
-    const bool boxed = BOXED && row0 + 32 <= t.p[0];
+    const int n = steps(t, w), col = col0(t, w) + w.lane;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int c = w.half * (kBN / 2) + 32 * i, col = t.b_mn + c;
+      const int r0 = 32 * (2 * i + w.half), row0 = t.b_mn + r0, rows = min(32, t.p[0] - r0);
       float d[32];
       if constexpr (ACT == kActNone) {
-        load_acc32(taddr + c, d);
-        if (kParts && part) {
-          if (valid) {
-            float4* dst = reinterpret_cast<float4*>(part + ((int64_t)t.p[1] * M_total + row) * K + col);
+        load_acc32(taddr + r0, d);
+        if (part) {
+          float* dst = part + ((int64_t)t.p[1] * M_total + row0) * K + col;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
-          }
-        } else if (boxed) {
+          for (int r = 0; r < 32; ++r)
+            if (r < rows) dst[(int64_t)r * K] = d[r];
+        } else if (rows == 32) {
           w.free_boxes();
-          put_row(w.base, w.lane, d);
+#pragma unroll
+          for (int r = 0; r < 32; ++r) put(at(w.base, r, w.lane), d[r]);
           w.publish();
           if (w.lane == 0) {
             ptx::tma_store_3d(&w.maps->c[0], w.base, col, row0, 0);
             ptx::bulk_commit();
           }
-        } else if (valid) {
-          gg::store_row32(dA + (int64_t)row * K + col, d);
+        } else {
+          __nv_bfloat16* dst = dA + (int64_t)row0 * K + col;
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            if (r < rows) dst[(int64_t)r * K] = __float2bfloat16_rn(d[r]);
         }
       } else {
-        const int slot = kGu == 2 ? i & 1 : 0;
-        const int64_t at = (int64_t)row * 2 * K + col;
-        const uint32_t box = w.base + 2048 + slot * 4096;
-        if constexpr (BOXED) {
-          w.free_boxes();
-          if (kGu == 2 ? i + 1 < n : i > 0) load_gu(t, w, kGu == 2 ? i + 1 : i);
-        }
-        load_acc32(taddr + c, d);
+        const uint32_t gbox = w.base + 2048 + (i & 1) * 4096, ubox = gbox + 2048;
+        w.free_boxes();
+        if (i + 1 < n) load_gu(t, w, i + 1);
+        load_acc32(taddr + r0, d);
+        turn(w.base, w.lane, d);
         float g[32], u[32];
-        if constexpr (BOXED) {
-          if (!w.wait(slot)) return false;
-          get_row(box, w.lane, g);
-          get_row(box + 2048, w.lane, u);
-        } else if (valid) {
-          load_row32(gu + at, g);
-          load_row32(gu + at + K, u);
-        }
+        if (!w.wait(i & 1)) return false;
+        get_half(gbox, w.lane, g);
+        get_half(ubox, w.lane, u);
 #pragma unroll
         for (int q = 0; q < 32; ++q) {
           float a, da;
@@ -223,21 +223,29 @@ struct RowGrad {
           d[q] *= a;
           u[q] *= a;
         }
-        if (boxed) {
-          put_row(box, w.lane, g);
-          put_row(box + 2048, w.lane, d);
-          if (h) put_row(w.base, w.lane, u);
+        const int c0 = col - w.lane;
+        if (rows == 32) {
+          __syncwarp();  // every lane has its part of d: h takes its place
+          put_half(gbox, w.lane, g);
+          put_half(ubox, w.lane, d);
+          if (h) put_half(w.base, w.lane, u);
           w.publish();
           if (w.lane == 0) {
-            ptx::tma_store_3d(&w.maps->c[0], box, col, row0, 0);
-            ptx::tma_store_3d(&w.maps->c[0], box + 2048, K + col, row0, 0);
-            if (h) ptx::tma_store_3d(&w.maps->c[2], w.base, col, row0, 0);
+            ptx::tma_store_3d(&w.maps->c[0], gbox, c0, row0, 0);
+            ptx::tma_store_3d(&w.maps->c[0], ubox, K + c0, row0, 0);
+            if (h) ptx::tma_store_3d(&w.maps->c[2], w.base, c0, row0, 0);
             ptx::bulk_commit();
           }
-        } else if (valid) {
-          gg::store_row32(dA + at, g);
-          gg::store_row32(dA + at + K, d);
-          if (h) gg::store_row32(h + (int64_t)row * K + col, u);
+        } else {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int r = w.lane / 2 + p / 2 * 16, c = c0 + (w.lane & 1) * 16 + p % 2 * 8;
+            if (r >= rows) continue;
+            __nv_bfloat16* dst = dA + (int64_t)(row0 + r) * 2 * K + c;
+            *reinterpret_cast<uint4*>(dst) = pack8(g + 8 * p);
+            *reinterpret_cast<uint4*>(dst + K) = pack8(d + 8 * p);
+            if (h) *reinterpret_cast<uint4*>(h + (int64_t)(row0 + r) * K + c) = pack8(u + 8 * p);
+          }
         }
       }
     }
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(256)
 // Experts without rows get zeros (or are left as they are when adding).
 template <bool F32, bool ADD>
 struct WeightGrad {
-  static constexpr bool kAMn = true, kBMn = true, kTail = true;
+  static constexpr bool kAMn = true, kBMn = true, kTail = true, kVarN = false;
   static constexpr int kBN = 256, kFmt = 1, kChunk = F32 ? 12 : 64;
   static constexpr int kStageWarp = 2048, kSharedInts = gg::kMaxE + 1;
 
@@ -410,74 +418,55 @@ inline int sum_parts(int64_t units, int64_t tiles, int64_t nkb, int64_t part_byt
 
 cudaError_t launch_grouped_dgrad(const void* dC, const void* B, const int32_t* offsets, int M_total,
                                  int E, int N, int K, int act, const void* gu, void* dA, void* h,
-                                 int max_rows_per_expert, int32_t* status, void* scratch, size_t scratch_bytes,
-                                 cudaStream_t s, const char** why) {
+                                 int32_t* status, void* scratch, size_t scratch_bytes, cudaStream_t s,
+                                 const char** why) {
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int64_t out_cols = act == kActNone ? K : 2 * (int64_t)K;
-  // Pairs where they pay for their second launch, of the experts' last rows: 256
-  // rows an expert over many waves of tiles, or 1024 over a few. (us, pairs and
-  // singles: 16384 rows of 4 experts, N = K = 4096, 408 and 423; of 64, N = 2048,
-  // K = 7168, 588 and 624; 8192 rows of 16, N = 7168, K = 2048, 4 waves, 241 and
-  // 208; 4096 of 4, N = K = 4096, 125 and 112; 4096 of 64, 401 and 349.)
-  const int most = max_rows_per_expert > 0 ? std::min(max_rows_per_expert, M_total) : M_total;
-  const int64_t each = M_total / E, all = ((int64_t)M_total / mm::BM + E / 2) * ceil_div(K, 256);
-  const bool many = most > mm::BM && each >= 256 &&
-                    (all >= 16 * (int64_t)num_sms() || (each >= 1024 && M_total >= 8192 && all >= 4 * (int64_t)num_sms()));
-  const int64_t tiles_ub = ((int64_t)M_total / mm::BM + std::min(M_total, E)) * ceil_div(K, 256);
-  const int parts = mm::sum_parts(num_sms(), tiles_ub, N / mm::BK, (int64_t)M_total * K * 4, scratch_bytes);
-  const bool pairs = many && parts == 1;
-  // (in parts, the tiles' results go to the scratch, by plain stores)
-  mm::Maps single = {}, pair = {};
-  bool ok = mm::make_operand(&single.a, dC, true, M_total, N, false, mm::BM) &&
-            mm::make_operand(&single.b, B, true, (int64_t)E * N, K, true, 256) &&
-            mm::make_boxes(&single.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) &&
-            (!gu || mm::make_boxes(&single.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) &&
-            (!h || mm::make_boxes(&single.c[2], h, bf16, 2, 1, M_total, K, 64));
-  if (pairs) {
-    pair = single;
-    ok = ok && mm::make_operand(&pair.b, B, true, (int64_t)E * N, K, true, 128);
-  }
-  if (!ok) {
+  const int cg = K > 128 ? 2 : 1, cols = mm::BM * cg;
+  const int bn = cg == 2 && M_total <= 32 * (int64_t)E ? 64 : 128 * cg;  // (RowGrad says why)
+  const int64_t tiles = ((int64_t)M_total / bn + std::min(M_total, E)) * ceil_div(K, cols);  // at most
+  const int parts = mm::sum_parts(num_sms() / cg, tiles, N / mm::BK, (int64_t)M_total * K * 4, scratch_bytes);
+  mm::Maps maps = {};
+  if (!mm::make_operand(&maps.a, B, true, (int64_t)E * N, K, true, mm::BM) ||
+      !mm::make_operand(&maps.b, dC, true, M_total, N, false, bn / cg) ||
+      !mm::make_operand(&maps.b_few, dC, true, M_total, N, false, mm::kFew) ||
+      !mm::make_boxes(&maps.c[0], dA, bf16, 2, 1, M_total, out_cols, 64) ||
+      (gu && !mm::make_boxes(&maps.c[1], gu, bf16, 2, 1, M_total, out_cols, 64)) ||
+      (h && !mm::make_boxes(&maps.c[2], h, bf16, 2, 1, M_total, K, 64))) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  auto go = [&](auto op, auto cg, mm::RowSet set) {
-    constexpr int CG = decltype(cg)::value;
+  auto go = [&](auto op, auto cg_c) {
+    constexpr int CG = decltype(cg_c)::value;
     op.offsets = offsets;
     op.E = E;
     op.M_total = M_total;
     op.N = N;
     op.K = K;
-    op.NT = (int)ceil_div(K, op.kBN);
-    op.band = 16 / CG;
-    op.set = set;
+    op.NT = (int)ceil_div(K, op.kCols);
     op.parts = parts;
     op.part = parts > 1 ? static_cast<float*>(scratch) : nullptr;
-    op.gu = static_cast<const __nv_bfloat16*>(gu);
     op.dA = static_cast<__nv_bfloat16*>(dA);
     op.h = static_cast<__nv_bfloat16*>(h);
-    const int64_t tiles = ((int64_t)M_total / op.kRows + std::min(M_total, E)) * op.NT * parts;
-    return mm::launch<decltype(op), CG>(CG == 2 ? pair : single, op, tiles, status, s);
+    return mm::launch<decltype(op), CG>(maps, op, tiles * parts, status, s);
   };
   auto both = [&](auto act_c) {
     constexpr int ACT = decltype(act_c)::value;
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
-    if (parts > 1) {
-      cudaError_t e = go(mm::RowGrad<kActNone, false, true>{}, One{}, mm::kAllRows);
-      if (e != cudaSuccess) return e;
-      const dim3 grid((unsigned)ceil_div(M_total, 8), (unsigned)ceil_div(K, 1024));
-      return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, 1, static_cast<const float*>(scratch), parts,
-                                   offsets, E, M_total, K, static_cast<const __nv_bfloat16*>(gu),
-                                   static_cast<__nv_bfloat16*>(dA), static_cast<__nv_bfloat16*>(h));
-    }
-    if (pairs) {
-      cudaError_t e = go(mm::RowGrad<ACT, true, true>{}, Two{}, mm::kPairRows);
-      if (e != cudaSuccess) return e;
-    }
-    const mm::RowSet rows = pairs ? mm::kRestRows : mm::kAllRows;
-    return ACT == kActNone || N < 4096 ? go(mm::RowGrad<ACT, false, true>{}, One{}, rows)
-                                       : go(mm::RowGrad<ACT, false, ACT == kActNone>{}, One{}, rows);
+    auto product = [&](auto a) {
+      constexpr int A = decltype(a)::value;
+      return bn == 64  ? go(mm::RowGrad<A, 2, 64>{}, Two{})
+             : cg == 2 ? go(mm::RowGrad<A, 2, 256>{}, Two{})
+                       : go(mm::RowGrad<A, 1, 128>{}, One{});
+    };
+    if (parts == 1) return product(act_c);
+    cudaError_t e = product(std::integral_constant<int, kActNone>{});
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)ceil_div(M_total, 8), (unsigned)ceil_div(K, 1024));
+    return mm::launch_overlapped(mm::sum_rows_kernel<ACT>, grid, 256, s, 1, static_cast<const float*>(scratch), parts,
+                                 offsets, E, M_total, K, static_cast<const __nv_bfloat16*>(gu),
+                                 static_cast<__nv_bfloat16*>(dA), static_cast<__nv_bfloat16*>(h));
   };
   switch (act) {
     case kActSilu: return both(std::integral_constant<int, kActSilu>{});

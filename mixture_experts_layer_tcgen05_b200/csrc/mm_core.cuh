@@ -33,6 +33,8 @@
 //   kAMn, kBMn    operand stored with MN along memory
 //   kBN           tile columns;  kFmt  1 bf16, 0 fp16
 //   kTail         tiles may end inside a k block (both operands MN-major)
+//   kVarN         a tile has Tile::n <= kBN columns, a multiple of 16: the MMA takes
+//                 time in proportion down to about 128
 //   kChunk        k blocks summed by the MMA at a time, 0: all
 //   kStageWarp    bytes of staging per epilogue warp (a multiple of 1024)
 //   kSharedInts   int32 words of shared memory for its tables
@@ -59,6 +61,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTileA = BM * BK * 2;         // 16 KB
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kFew = 32;                    // kVarN: rows of the smaller box of b
 constexpr int kBarBytes = 512;
 constexpr int kSiteTail = 9;                // status word: the tail-zeroing wait,
 constexpr int kSiteLoad = 10;               // an epilogue warp's wait for its own loads
@@ -68,6 +71,7 @@ struct Tile {
   int b_mn, b_k;
   int nkb;        // k blocks; 0: the accumulator is zero and is not read
   int tail;       // valid k rows of the last block (1..64)
+  int n;          // kVarN: columns
   int p[3];       // the Op's own
 };
 
@@ -90,6 +94,7 @@ struct Cfg {
   static_assert(kTileB % 1024 == 0, "B tiles are whole swizzle atoms");
   static_assert(!Op::kBMn || kBRows % 64 == 0, "MN-major boxes are 64 wide");
   static_assert(!Op::kTail || (Op::kAMn && Op::kBMn), "a ragged sum needs rows as k");
+  static_assert(!Op::kVarN || (!Op::kBMn && !Op::kTail && Op::kChunk == 0 && kBRows >= kFew), "rows of a K-major b");
   static_assert(STAGES >= 2, "shared memory of one CTA");
 };
 
@@ -101,7 +106,7 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* tm
     if constexpr (CG == 2) ptx::tma_load_3d_pair(dst, tm, 0, k, mn / 64, bar);
     else ptx::tma_load_3d(dst, tm, 0, k, mn / 64, bar);
   } else {
-    static_assert(ROWS == 128, "one box of rows");
+    static_assert(ROWS == 128 || ROWS == kFew, "one box of rows");
     if constexpr (CG == 2) ptx::tma_load_2d_pair(dst, tm, k, mn, bar);
     else ptx::tma_load_2d(dst, tm, k, mn, bar);
   }
@@ -140,7 +145,8 @@ struct Ring {
 
 struct Maps {
   CUtensorMap a, b;
-  CUtensorMap c[3];  // the epilogue's own
+  CUtensorMap b_few;  // kVarN: b in boxes of kFew rows
+  CUtensorMap c[3];   // the epilogue's own
 };
 
 // An epilogue warp: which part of the tile it holds, and its staging, boxes of
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The producer's and the MMA issuer's loops run in one warp each, so a k block
   // costs them their instructions' latencies: positions in the ring are stepped,
   // not divided out (measured without loads: a loop with 64-bit quotients took 675
-  // cycles a block, whatever the MMA's size, and 593 without them; @N with the
+  // cycles a block, whatever the MMA's size, and 593 without them; 558 with the
   // whole warp in the loop; the MMAs themselves take 512).
   if (warp == 0) {
     // The whole warp walks the tiles and waits, one lane loads.
@@ -297,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<STAGES, C::kStage> at(sbase);
     bool ok = true;
     for (int tile = unit0; tile < total && ok; tile = next(tile)) {
-      const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * C::kBRows;
+      const int am = t.a_mn + rank * BM, bn = t.b_mn + rank * (Op::kVarN ? t.n / CG : C::kBRows);
+      const bool few = Op::kVarN && t.n <= kFew * CG;  // of this CTA's rows of b
       int ka = t.a_k, kbb = t.b_k;
       for (int left = t.nkb; left > 0; --left, ka += BK, kbb += BK) {
         if (!ptx::mbar_wait(empty0 + at.bar, at.parity ^ 1, status, kSiteProducerEmpty)) {
@@ -310,12 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = tail0 + at.bar;  // this CTA's warp 2 waits for the bytes and arrives on `full` itself
             ptx::mbar_arrive_expect_tx(bar, C::kStage);
           } else {
+            const uint32_t bytes = few ? kTileA + kFew * 128 : C::kStage;
             bar = lead_full0 + at.bar;
-            if (CG == 2 && rank != 0) ptx::mbar_arrive_expect_tx_cluster(bar, C::kStage);
-            else ptx::mbar_arrive_expect_tx(full0 + at.bar, C::kStage);
+            if (CG == 2 && rank != 0) ptx::mbar_arrive_expect_tx_cluster(bar, bytes);
+            else ptx::mbar_arrive_expect_tx(full0 + at.bar, bytes);
           }
           load_operand<Op::kAMn, BM, CG>(at.stage, &maps.a, am, ka, bar);
-          load_operand<Op::kBMn, C::kBRows, CG>(at.stage + kTileA, &maps.b, bn, kbb, bar);
+          load_operand<Op::kBMn, C::kBRows, CG>(at.stage + kTileA, few ? &maps.b_few : &maps.b, bn, kbb, bar);
         }
         at.step();
       }
@@ -342,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 16 k further: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
       constexpr uint64_t stepA = Op::kAMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
       constexpr uint64_t stepB = Op::kBMn ? (UK * 128) >> 4 : (UK * 2) >> 4;
+      uint32_t idesc = C::kIdesc;
       auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t more) {
-        if constexpr (CG == 2) ptx::mma_f16_pair(d, da, db, C::kIdesc, more);
-        else ptx::mma_f16(d, da, db, C::kIdesc, more);
+        if constexpr (CG == 2) ptx::mma_f16_pair(d, da, db, idesc, more);
+        else ptx::mma_f16(d, da, db, idesc, more);
       };
       auto commit = [&](uint32_t bar) {
         if constexpr (CG == 2) ptx::mma_commit_pair(bar);
@@ -352,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int tile = unit0; tile < total && ok; tile = next(tile)) {
         int left = t.nkb;
+        if constexpr (Op::kVarN) idesc = (C::kIdesc & ~(63u << 17)) | (uint32_t)(t.n >> 3) << 17;
         do {  // once without chunks; an empty sum still hands over its (unread) accumulator
           if (!ptx::mbar_wait(acce0 + acc * 8, acc_ph ^ 1, status, kSiteMmaAccEmpty)) {
             ok = false;

@@ -82,7 +82,7 @@ enum SquareMode { kGram, kPart, kPoly };
 template <bool MN, SquareMode MODE, int SIDE>
 struct Square {
   static constexpr bool POLY = MODE == kPoly;
-  static constexpr bool kAMn = MN, kBMn = MN, kTail = false;
+  static constexpr bool kAMn = MN, kBMn = MN, kTail = false, kVarN = false;
   static constexpr int kBN = SIDE, kFmt = 0, kChunk = 0;
   static constexpr int kStageWarp = POLY ? 8192 : 4096, kSharedInts = 0;
 
@@ -211,7 +211,7 @@ struct Square {
 // X <- a X + B X (LEFT) or a X + X B.
 template <bool LEFT, int SIDE>
 struct Apply {
-  static constexpr bool kAMn = false, kBMn = LEFT, kTail = false;
+  static constexpr bool kAMn = false, kBMn = LEFT, kTail = false, kVarN = false;
   static constexpr int kBN = SIDE, kFmt = 0, kChunk = 0;
   static constexpr int kStageWarp = 8192, kSharedInts = 0;
 
@@ -818,7 +818,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       op.nkb = (int)(k / BK);
       op.parts = cuts;
       op.tiles = (int)square_tiles(P.pp, SIDE);
-      const Maps maps = {tm, tm, {result, g_io, g_io}};
+      const Maps maps = {tm, tm, tm, {result, g_io, g_io}};
       return launch<decltype(op), CG>(maps, op, (int64_t)nb * op.tiles * cuts, status, s, true);
     };
     for (int i = 0; i < steps; ++i) {
@@ -839,7 +839,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       op.nkb = (int)(P.pp / BK);
       op.mt = (int)ceil_div(P.mp, SIDE);
       op.nt = (int)ceil_div(P.np, SIDE);
-      const Maps maps = {LEFT ? pk : xk[in], LEFT ? xmn[in] : pk,
+      const Maps maps = {LEFT ? pk : xk[in], LEFT ? xmn[in] : pk, pk,
                          {st.from_g ? g_in : xh_io[in], xl_io, st.last ? o_out : xh_io[in ^ 1]}};
       e = launch<decltype(op), CG>(maps, op, (int64_t)nb * op.mt * op.nt, status, s, true);
       if (e != cudaSuccess) return e;

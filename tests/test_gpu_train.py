@@ -132,11 +132,12 @@ def test_dgrad(counts, N, K, act, with_h):
         within(h.t[:R], ref, ref.abs() * 2.0**-8 + 2.0**-18 * (1 + g.abs()) * (g * u).abs(), "h")
 
 
-@pytest.mark.parametrize("bound", [0, 16, 32, 64, 1000])
 @pytest.mark.parametrize("act", [moe.MOE_EPILOGUE_NONE, moe.MOE_EPILOGUE_SWIGLU])
-@pytest.mark.parametrize("counts", [[1, 0, 9, 16], [0, 33, 64, 5], [70, 1, 0, 130]])
-def test_dgrad_row_bounds(counts, act, bound):
-    """Every bound on the rows gives the same result, also one that the rows exceed."""
+@pytest.mark.parametrize("counts", [[1, 0, 9, 16], [0, 33, 64, 5], [70, 1, 0, 130], [257, 31, 32, 33], [511, 513],
+                                    [48, 240, 250, 272], [2049, 15], [4200],
+                                    [200, 0, 0, 0, 1, 3, 0, 0], [0, 65, 0, 0, 31, 33, 64]])
+def test_dgrad_row_tiles(counts, act):
+    """Row counts around the sizes that tiles, their groups of rows and the small boxes end at."""
     E, R, N, K = len(counts), sum(counts), 640, 384
     gen = _gen(R + act)
     dC, B = _randn(gen, R, N), _randn(gen, E, N, K, std=0.05)
@@ -145,8 +146,7 @@ def test_dgrad_row_bounds(counts, act, bound):
     out = torch.full((R, 2 * K if gated else K), float("nan"), dtype=BF16, device="cuda")
     h = torch.full((R, K), float("nan"), dtype=BF16, device="cuda") if gated else None
     ws = _ws(1 << 22)
-    moe.moe_grouped_gemm_dgrad(dC, B, _offsets(counts), R, E, N, K, act, out, gu=gu, h=h, ws=ws,
-                               max_rows_per_expert=bound)
+    moe.moe_grouped_gemm_dgrad(dC, B, _offsets(counts), R, E, N, K, act, out, gu=gu, h=h, ws=ws)
     assert moe.moe_get_device_status(ws) == 0
     d, eps = rows64(dC, B, counts)
     if not gated:
