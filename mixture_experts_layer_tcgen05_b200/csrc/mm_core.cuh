@@ -580,6 +580,19 @@ inline bool make_boxes(CUtensorMap* m, const void* base, CUtensorMapDataType dt,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// set_smem once per device (a bit of `sized` each): a fifth of a launch's host time.
+template <class K>
+inline cudaError_t set_smem_once(std::atomic<uint64_t>& sized, K k, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (sized.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = set_smem(k, bytes);
+  if (e == cudaSuccess) sized.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // overlap: the kernel may start (its set-up, up to wait_for_previous_grid)
 // while the one ahead of it in the stream still runs.
 // (static: were `sized` shared between two copies of this library in a process,
@@ -589,17 +602,9 @@ static cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t
                           bool overlap = false) {
   using C = Cfg<Op, CG>;
   auto k = mm_kernel<Op, CG>;
-  // once per device: a fifth of a launch's host time
   static std::atomic<uint64_t> sized{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = set_smem_once(sized, k, C::kSmem);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!bit || !(sized.load(std::memory_order_relaxed) & bit)) {
-    e = set_smem(k, C::kSmem);
-    if (e != cudaSuccess) return e;
-    sized.fetch_or(bit, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
@@ -628,11 +633,12 @@ static cudaError_t launch(const Maps& maps, const Op& op, int64_t tiles, int32_t
 // A plain kernel that starts with wait_for_previous_grid, launched to overlap;
 // its blocks in clusters of `cluster`.
 template <typename... Par, typename... Arg>
-inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned threads, cudaStream_t s, unsigned cluster,
-                                     Arg... args) {
+inline cudaError_t launch_overlapped_smem(void (*k)(Par...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                                          unsigned cluster, Arg... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -646,6 +652,12 @@ inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned thre
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
+}
+
+template <typename... Par, typename... Arg>
+inline cudaError_t launch_overlapped(void (*k)(Par...), dim3 grid, unsigned threads, cudaStream_t s, unsigned cluster,
+                                     Arg... args) {
+  return launch_overlapped_smem(k, grid, threads, 0, s, cluster, args...);
 }
 
 }  // namespace mm

@@ -368,6 +368,15 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
+// 1 / (|G|_F + eps), from the sum of squares, as x y, x a power of two near 1 /
+// |G|_F: the norm of entries near fp32's largest has an inverse below fp32's
+// smallest normal.
+__device__ __forceinline__ float2 inverse_norm(double sum, float eps) {
+  const double norm = sqrt(sum);
+  const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
+  return make_float2((float)p2, (float)(1.0 / (norm * p2 + (double)eps * p2)));
+}
+
 // part[b][chunk] = the sum of squares of a chunk of matrix b, in fp64 (squares
 // of any fp32 value fit, and the sum has no rounding to speak of).
 template <typename T>
@@ -407,11 +416,8 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const
   const int64_t b = blockIdx.y;
   double v = 0.0;
   for (int i = threadIdx.x; i < chunks; i += kNormThreads) v += part[b * chunks + i];
-  // 1 / (|G|_F + eps) as p r, p a power of two near 1 / |G|_F: the norm of
-  // entries near fp32's largest has an inverse below fp32's smallest normal
-  const double norm = sqrt(block_sum(v));
-  const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
-  const float p = (float)p2, r = (float)(1.0 / (norm * p2 + (double)eps * p2));
+  const float2 f = inverse_norm(block_sum(v), eps);
+  const float p = f.x, r = f.y;
   if (blockIdx.x == 0 && threadIdx.x == 0) inv[b] = make_float2(p, r);
   const T* src = static_cast<const T*>(st.g) + b * st.rows * st.cols;
   const int64_t base = b * st.mp * st.np;
@@ -600,9 +606,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   sync();
   s = 0.0;
   for (int r = 0; r < CLUSTER; ++r) s += CLUSTER > 1 ? peer_f64(&norm_of, r) : norm_of;
-  const double norm = sqrt(s);
-  const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
-  const float f = (float)p2, inv = (float)(1.0 / (norm * p2 + (double)eps * p2));
+  const float2 factors = inverse_norm(s, eps);
+  const float f = factors.x, inv = factors.y;
 
   // step -1 takes G; step i < steps - 1 leaves A of the one after it
 #pragma unroll 1
@@ -677,6 +682,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   }
   // (the last peer reads are behind a barrier of every step; with steps >= 1 there was one)
 }
+
+}  // namespace mm
+}  // namespace moe
+
+#include "orthogonalize_short.cuh"
+
+namespace moe {
+namespace mm {
 
 struct OrthPlan {
   int64_t mp, np, pp, chunks;
@@ -766,6 +779,32 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
     if (p <= 2) return sized(std::integral_constant<int, 2>{});
     if (p <= 4) return sized(std::integral_constant<int, 4>{});
     return sized(std::integral_constant<int, 8>{});
+  }
+  if (is_short(rows, cols)) {
+    ShortArgs args;
+    args.g = g;
+    args.out = st.out;
+    args.status = status;
+    args.p = std::min(rows, cols);
+    args.q = std::max(rows, cols);
+    const int cluster = short_cluster(stack, args.q);
+    args.slice = (int)align_up(ceil_div(args.q, cluster), 64);
+    args.steps = steps;
+    args.g_f32 = g_f32;
+    args.wide = rows <= cols;
+    args.s = st.s;
+    args.inv_s = st.inv_s;
+    args.a = a;
+    args.b = b;
+    args.c = c;
+    args.eps = eps;
+    args.scale = scale;
+    switch (cluster) {
+      case 1: return launch_short<1>(args, nb, s);
+      case 2: return launch_short<2>(args, nb, s);
+      case 4: return launch_short<4>(args, nb, s);
+      default: return launch_short<8>(args, nb, s);
+    }
   }
   const dim3 ngrid((unsigned)P.chunks, (unsigned)nb);
   const int64_t vecs = P.mp * P.np / 8;

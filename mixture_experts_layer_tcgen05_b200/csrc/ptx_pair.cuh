@@ -1,5 +1,6 @@
 // Thin inline-PTX wrappers that the training kernels use beside ptx.cuh's:
-// operands whose MN index runs along memory, and MMAs over a pair of CTAs.
+// operands whose MN index runs along memory, TMEM written by threads, and MMAs
+// over a pair of CTAs.
 #pragma once
 
 #include "ptx.cuh"
@@ -63,6 +64,19 @@ __device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32
           reinterpret_cast<uint64_t>(tmap)),
       "r"(c0), "r"(c1), "r"(c2), "r"(src)
       : "memory");
+}
+
+// tmem_ld16's columns written back.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // A kernel launched with programmatic stream serialisation may start before
