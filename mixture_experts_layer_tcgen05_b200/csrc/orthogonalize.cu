@@ -28,6 +28,9 @@
 // reach from 1 / sqrt(p q) to 1, and those of A from 1 / (p sqrt(q)) to 1. The
 // norm is summed in fp64.
 //
+// Three forms: p <= 8 on the FMA units (narrow_kernel), p <= 128 in one launch
+// (orthogonalize_short.cuh), and this file's launches over MMA tiles.
+//
 // Work per step and matrix: p^2 q MACs for A and p^3 for A^2, each symmetric
 // and computed for its upper tiles only (the epilogue stores a tile and its
 // mirror image), and p^2 q for B X.
@@ -790,6 +793,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
     const int cluster = short_cluster(stack, args.q);
     args.slice = (int)align_up(ceil_div(args.q, cluster), 64);
     args.steps = steps;
+    args.own = (int)align_up(ceil_div(args.p, cluster), 8);
     args.g_f32 = g_f32;
     args.wide = rows <= cols;
     args.s = st.s;

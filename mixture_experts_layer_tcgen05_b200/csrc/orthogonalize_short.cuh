@@ -8,14 +8,24 @@
 // swizzled. Both products read that one copy, A = X X^T with the columns as k
 // (K-major), B X with the rows as k (MN-major). The lower halves are in TMEM,
 // two columns of X to a TMEM column. A step:
-//   - the CTA's part of A by MMA, in fp32 to shared memory; cluster barrier;
-//     each CTA adds 128 / C rows of the parts, in order, and writes them as fp16
-//     into the A of every CTA; cluster barrier;
+//   - the CTA's part of A by MMA, in fp32 to shared memory; `own` rows of it to
+//     each CTA by bulk copy; each adds what it got, in order, and copies its rows of
+//     A, in fp16, to the others. The copies complete on barriers of the receiving
+//     CTA, and each stage's data is only sent when all of the one before has come, so
+//     nothing else keeps the buffers apart. (Loads of the other CTAs' memory, stores
+//     to it and two cluster barriers took 10200 cycles a step instead of 6200.)
 //   - A^2 by MMA and B = b A + c A^2 in every CTA alike, over its own part of A;
 //   - B X by MMA, 128 columns at a time into two accumulators in turn, and
 //     X <- a X + B X in place: a chunk's MMAs read that chunk's columns alone.
-// Bound by latency: the MMAs are a tenth of the time, the rest waits for them, the
-// barriers and the other CTAs' shared memory. @T
+// Bound by latency. Of a step's 12700 cycles (128 x 128 to a CTA, four CTAs) the
+// issue of the 24 MMAs takes 2500, the exchange of A 6200 (a third of it the copies'
+// bytes, 48 KB each way) and the epilogues 3700; before the first step 13000 go to
+// reading G and its norm. Measured, against the launches of the general form: eight
+// 512 x 128 43 and 84 us, one 128 x 128 28 and 74, 16 x 512 25 and 67, 100 x 2000 57
+// and 95, a thousand 128 x 128 199 and 648, 64 of 2048 x 128 316 and 339. A CTA's
+// slice is at most the 256 columns that shared memory has room for beside the parts of
+// A (at 512 columns and with the loads of the others' memory, one 128 x 4096 was no
+// faster than the general form), so longer sides than 8 x 256 are the general form's.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -25,8 +35,9 @@
 namespace moe {
 namespace mm {
 
-constexpr int kShort = 128, kShortSlice = 512, kShortThreads = 256, kShortMost = 8;  // p, columns of a CTA, CTAs
-constexpr size_t kShortSmem = 1024 + kShortSlice * 256 + 3 * 32768;  // X, A, and the part of A that B replaces
+constexpr int kShort = 128, kShortSlice = 256, kShortThreads = 256, kShortMost = 8;  // p, columns of a CTA, CTAs
+// X, A, the part of A (which B replaces), and the parts that others sent
+constexpr size_t kShortSmem = 1024 + kShortSlice * 256 + 32768 + 2 * 65536;
 constexpr int kShortLow = 256;  // TMEM: two accumulators of 128 columns, then the lower halves
 
 struct ShortArgs {
@@ -34,6 +45,7 @@ struct ShortArgs {
   __nv_bfloat16* out;    // likewise
   int32_t* status;
   int p, q, slice, steps;
+  int own;               // rows of A that a CTA adds, a multiple of 8: CTA r those from r own, if below p
   bool g_f32, wide;
   float s, inv_s, a, b, c, eps, scale;
 };
@@ -51,29 +63,10 @@ __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 16 bytes at `addr` of CTA `rank`'s shared memory
-template <int C>
-__device__ __forceinline__ uint4 peer_get(uint32_t addr, int rank) {
-  if constexpr (C == 1) return Warp::get(addr);
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(ptx::map_to_cta(addr, rank))
-               : "memory");
-  return v;
-}
-template <int C>
-__device__ __forceinline__ void peer_put(uint32_t addr, int rank, uint4 v) {
-  if constexpr (C == 1) return Warp::put(addr, v);
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::map_to_cta(addr, rank)), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 template <int C>
 __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2];
+  __shared__ alignas(8) uint64_t bars[4];  // two accumulators, parts of A, rows of A
   __shared__ uint32_t tmem_of;
   __shared__ double norm_of;
   __shared__ float rest[kShort];
@@ -81,7 +74,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   const int half = warp >> 2, row = (warp & 3) * 32 + lane;
   const int rank = C > 1 ? (int)ptx::cluster_ctarank() : 0, item = (int)blockIdx.x / C;
   const uint32_t x_at = (ptx::smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t a_at = x_at + kShortSlice * 256, part_at = a_at + 32768, b_at = part_at;
+  const uint32_t a_at = x_at + kShortSlice * 256, part_at = a_at + 32768, got_at = part_at + 65536, b_at = part_at;
   const uint32_t bar = ptx::smem_addr(bars);
   const bool used = (warp & 3) * 32 < o.p;  // the warp has rows of the matrix
   const int first = rank * o.slice, groups = o.slice / 32;
@@ -90,8 +83,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
 
   ptx::let_next_grid_start();
   if (tid == 0) {
-    ptx::mbar_init(bar, 1);
-    ptx::mbar_init(bar + 8, 1);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(bar + 8 * i, 1);
     ptx::fence_barrier_init();
   }
   if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&tmem_of), 512);
@@ -132,11 +124,17 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       return;
     }
     const int64_t base = at + (o.wide ? (int64_t)row * o.q + col : (int64_t)col * o.p + row), step = o.wide ? 1 : o.p;
+    if (o.g_f32) {
+      const float* src = static_cast<const float*>(o.g) + base;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col + j < o.q)
-        v[j] = o.g_f32 ? __ldg(static_cast<const float*>(o.g) + base + j * step)
-                       : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(o.g) + base + j * step));
+      for (int j = 0; j < 32; ++j)
+        if (col + j < o.q) v[j] = __ldg(src + j * step);
+    } else {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(o.g) + base;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j < o.q) v[j] = __bfloat162float(__ldg(src + j * step));
+    }
   };
   // 32 columns of the state from local column c0: two halves, 16 words each
   auto put_state = [&](int c0, const float (&v)[32]) {
@@ -150,19 +148,33 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     ptx::tmem_st16(tmem + lanes + kShortLow + c0 / 2, lo);
   };
 
-  double s0 = 0.0, s1 = 0.0;
-  if (used)
-#pragma unroll 1
-    for (int i = half; i < groups; i += 2) {
-      float v[32];
-      load_g(32 * i, v);
+  // Sum of squares: 32 at a time in fp32, times a power of two that keeps them in
+  // its range, then in fp64. Up to 128 columns stay in registers meanwhile.
+  float v0[32], v1[32];
+  auto squares = [](const float(&v)[32]) {
+    float m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        s0 += (double)v[j] * (double)v[j];
-        s1 += (double)v[j + 1] * (double)v[j + 1];
-      }
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
+    const int e = min(126, max(-126, 127 - (int)(__float_as_uint(m) >> 23)));  // m 2^e is near 1
+    const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] = fmaf(v[j] * f, v[j] * f, s[j & 3]);
+    return ldexp((double)((s[0] + s[1]) + (s[2] + s[3])), -2 * e);
+  };
+  double sum = 0.0;
+  if (used) {
+#pragma unroll 1
+    for (int i = 4 + half; i < groups; i += 2) {
+      load_g(32 * i, v0);
+      sum += squares(v0);
     }
-  double sum = block_sum(s0 + s1);
+    load_g(32 * half, v0);
+    if (groups > 2 + half) load_g(64 + 32 * half, v1);
+    sum += squares(v0);
+    if (groups > 2 + half) sum += squares(v1);
+  }
+  sum = block_sum(sum);
   if constexpr (C > 1) {
     if (tid == 0) norm_of = sum;
     __syncwarp();
@@ -177,15 +189,20 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   }
   {
     const float2 inv = inverse_norm(sum, o.eps);
-    if (used)
-#pragma unroll 1
-      for (int i = half; i < groups; i += 2) {
-        float v[32];
-        load_g(32 * i, v);
+    auto init = [&](int c0, float(&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = inv.x * v[j] * inv.y * o.s;
-        put_state(32 * i, v);
+      for (int j = 0; j < 32; ++j) v[j] = inv.x * v[j] * inv.y * o.s;
+      put_state(c0, v);
+    };
+    if (used) {
+      init(32 * half, v0);
+      if (groups > 2 + half) init(64 + 32 * half, v1);
+#pragma unroll 1
+      for (int i = 4 + half; i < groups; i += 2) {
+        load_g(32 * i, v0);
+        init(32 * i, v0);
       }
+    }
   }
 
   bool ok = true;
@@ -207,12 +224,23 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   };
   constexpr uint32_t kSquare = ptx::make_idesc(128, 128, 0, 0);
   const int chunks = (o.slice + 127) / 128;
+  // The products, issued by thread 0. In the descriptors addresses count 16 bytes:
+  // 16 k further is 2 along a K-major row, a block of 64 columns further 1024.
+  auto issue_square = [&](uint32_t m, int n) {
+    const uint64_t d0 = ptx::sw128_kmajor_desc(m);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const uint64_t d = d0 + (k >> 2) * 1024 + (k & 3) * 2;
+      ptx::mma_f16(tmem, d, d, kSquare, k > 0);
+    }
+    ptx::mma_commit(bar);
+  };
   auto issue_chunk = [&](int j) {
-    const uint32_t d = ptx::make_idesc(128, o.slice - 128 * j >= 128 ? 128 : 64, 0, 0) | ptx::kIdescBMn;
-#pragma unroll 1
+    const uint32_t i = ptx::make_idesc(128, o.slice - 128 * j >= 128 ? 128 : 64, 0, 0) | ptx::kIdescBMn;
+    const uint64_t db = ptx::sw128_kmajor_desc(b_at), dx = ptx::sw128_mnmajor_desc(x_at + j * 32768, 16384);
+#pragma unroll 4
     for (int k = 0; k < ksteps; ++k)
-      ptx::mma_f16(tmem + (j & 1) * 128, ptx::sw128_kmajor_desc(b_at + (k >> 2) * 16384 + (k & 3) * 32),
-                   ptx::sw128_mnmajor_desc(x_at + j * 32768 + k * 2048, 16384), d, k > 0);
+      ptx::mma_f16(tmem + (j & 1) * 128, db + (k >> 2) * 1024 + (k & 3) * 2, dx + k * 128, i, k > 0);
     ptx::mma_commit(bar + 8 * (j & 1));
   };
   const float ci = o.c * o.inv_s;
@@ -220,14 +248,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
 #pragma unroll 1
   for (int step = 0; step < o.steps; ++step) {
     hand_over();
-    if (tid == 0) {
-#pragma unroll 1
-      for (int k = 0; k < o.slice / 16; ++k) {
-        const uint64_t d = ptx::sw128_kmajor_desc(x_at + (k >> 2) * 16384 + (k & 3) * 32);
-        ptx::mma_f16(tmem, d, d, kSquare, k > 0);
-      }
-      ptx::mma_commit(bar);
-    }
+    if (tid == 0) issue_square(x_at, o.slice / 16);
     __syncwarp();
     wait(0);
     if (used)
@@ -241,46 +262,50 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
                     make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
                                __float_as_uint(v[4 * u + 3])));
       }
-    ptx::tc_fence_before();
-    __syncwarp();
-    if constexpr (C > 1) ptx::cluster_sync();
-    else __syncthreads();
-    // rows [128 / C rank, + 128 / C): pieces of 8 columns
-#pragma unroll
-    for (int i = 0; i < 8 / C; ++i) {
-      const int r = rank * (kShort / C) + i * 16 + tid / 16, j = tid % 16;
-      if (r >= o.p) continue;
-      uint4 lo[C], hi[C];
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        lo[k] = peer_get<C>(short_part_at(part_at, r, 2 * j), k);
-        hi[k] = peer_get<C>(short_part_at(part_at, r, 2 * j + 1), k);
-      }
-      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        v[0] += __uint_as_float(lo[k].x), v[1] += __uint_as_float(lo[k].y);
-        v[2] += __uint_as_float(lo[k].z), v[3] += __uint_as_float(lo[k].w);
-        v[4] += __uint_as_float(hi[k].x), v[5] += __uint_as_float(hi[k].y);
-        v[6] += __uint_as_float(hi[k].z), v[7] += __uint_as_float(hi[k].w);
-      }
-      uint32_t h[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) h[u] = pack_half2(v[2 * u] * o.inv_s, v[2 * u + 1] * o.inv_s);
-#pragma unroll
-      for (int k = 0; k < C; ++k) peer_put<C>(short_at(a_at, r, j), k, make_uint4(h[0], h[1], h[2], h[3]));
+    const int mine = rank * o.own;  // first of the rows of A that this CTA adds
+    const bool adds = mine < o.p;
+    hand_over();
+    if (C > 1 && tid == 0) {
+      if (adds) ptx::mbar_arrive_expect_tx(bar + 16, (C - 1) * o.own * 512);
+      const int others = (o.p + o.own - 1) / o.own - adds;
+      if (others) ptx::mbar_arrive_expect_tx(bar + 24, others * o.own * 256);
     }
+    if (C > 1 && warp == 0 && lane < C && lane != rank && lane * o.own < o.p)
+      ptx::bulk_copy_to_cta(ptx::map_to_cta(got_at + rank * o.own * 512, lane), part_at + lane * o.own * 512, o.own * 512,
+                            ptx::map_to_cta(bar + 16, lane));
     __syncwarp();
-    if constexpr (C > 1) ptx::cluster_sync();
-    hand_over();  // (each SM's own proxies: A came through the generic one, from wherever)
-    if (tid == 0) {
+    if (adds) {
+      if (C > 1) wait(2);
 #pragma unroll 1
-      for (int k = 0; k < ksteps; ++k) {
-        const uint64_t d = ptx::sw128_kmajor_desc(a_at + (k >> 2) * 16384 + (k & 3) * 32);
-        ptx::mma_f16(tmem, d, d, kSquare, k > 0);
+      for (int i = tid; i < o.own * 16; i += kShortThreads) {
+        const int r = i / 16, j = i % 16;  // 8 columns of a row
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          const uint32_t from = k == rank ? part_at + mine * 512 : got_at + k * o.own * 512;
+          const uint4 lo = Warp::get(short_part_at(from, r, 2 * j)), hi = Warp::get(short_part_at(from, r, 2 * j + 1));
+          v[0] += __uint_as_float(lo.x), v[1] += __uint_as_float(lo.y);
+          v[2] += __uint_as_float(lo.z), v[3] += __uint_as_float(lo.w);
+          v[4] += __uint_as_float(hi.x), v[5] += __uint_as_float(hi.y);
+          v[6] += __uint_as_float(hi.z), v[7] += __uint_as_float(hi.w);
+        }
+        uint32_t h[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) h[u] = pack_half2(v[2 * u] * o.inv_s, v[2 * u + 1] * o.inv_s);
+        Warp::put(short_at(a_at, mine + r, j), make_uint4(h[0], h[1], h[2], h[3]));
       }
-      ptx::mma_commit(bar);
     }
+    if constexpr (C > 1) {
+      hand_over();
+      if (adds && warp < 2 && lane < C && lane != rank) {  // a warp for each of A's blocks of 64 columns
+        const uint32_t from = a_at + warp * 16384 + mine * 128;
+        ptx::bulk_copy_to_cta(ptx::map_to_cta(from, lane), from, o.own * 128, ptx::map_to_cta(bar + 24, lane));
+      }
+      __syncwarp();
+      if ((o.p + o.own - 1) / o.own > adds) wait(3);
+    }
+    hand_over();
+    if (tid == 0) issue_square(a_at, ksteps);
     __syncwarp();
     wait(0);
     if (used)
@@ -377,15 +402,17 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       }
     }
   }
-  // (no CTA reads or writes another's memory past the last step's second barrier)
+  // the others have what was sent to them
   ptx::tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (C > 1) ptx::cluster_sync();
+  else __syncthreads();
   ptx::tc_fence_after();
   if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
 // The fewest CTAs that hold a matrix; more, down to slices of 128 columns, while
-// they all find an SM.
+// they all find an SM (eight 512 x 128: 47 us with slices of 128 or 64, 62 with 256).
 inline int short_cluster(int64_t stack, int64_t q) {
   int c = 1;
   while (c * kShortSlice < q) c *= 2;

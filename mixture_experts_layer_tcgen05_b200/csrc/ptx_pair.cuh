@@ -110,6 +110,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Copies this CTA's shared memory to another's (shared::cluster addresses), the
+// bytes completing on a barrier there. Addresses and size are multiples of 16.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Arrive on a barrier given by its shared::cluster address, handing over
 // TMEM reads that tcgen05.fence orders, or shared memory that a proxy fence
 // has given to the async proxy of its own SM. (Nothing is read through the

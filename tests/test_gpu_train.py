@@ -478,6 +478,68 @@ def test_orthogonalize(nb, rows, cols, dtype):
     check_orth(orth(G), newton64(G, 5), 5)
 
 
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("nb,p,q", [(2, 9, 9), (1, 16, 64), (1, 31, 65), (1, 32, 511), (2, 33, 128), (1, 34, 1000),
+                                    (1, 60, 61), (2, 64, 513), (1, 65, 1025), (1, 72, 192), (3, 97, 97), (1, 104, 1536),
+                                    (1, 127, 2047), (1, 128, 2048), (1, 128, 2049), (1, 129, 512), (40, 20, 300),
+                                    (30, 128, 700), (160, 24, 257), (20, 100, 2000)])
+def test_orthogonalize_short_sides(nb, p, q, tall):
+    """Every size of cluster, rows that end inside a warp's or a CTA's share, slices that end past the matrix."""
+    G = _randn(_gen(p * 7 + q), nb, *((q, p) if tall else (p, q)), dtype=torch.float32 if q % 2 else BF16)
+    check_orth(orth(G), newton64(G, 5), 5)
+
+
+@pytest.mark.parametrize("shape", [(1, 100, 1800), (3, 640, 128), (1, 17, 600)])
+def test_orthogonalize_short_sides_of_low_rank(shape):
+    gen = _gen(17)
+    nb, m, n = shape
+    G = _randn(gen, nb, m, 3, dtype=torch.float32) @ _randn(gen, nb, 3, n, dtype=torch.float32)
+    check_orth(orth(G), newton64(G, 5), 5)
+
+
+def test_orthogonalize_short_sides_beside_other_kernels():
+    """Clusters that hold their SMs whole, on two streams with pairs of SMs that do likewise; captured, too."""
+    R, N, K = 3000, 512, 512
+    gen = _gen(23)
+    dC, A, off = _randn(gen, R, N), _randn(gen, R, K), _offsets([R])
+    G, H = _randn(gen, 20, 96, 1000, dtype=torch.float32), _randn(gen, 2, 700, 128, dtype=torch.float32)
+
+    def run(spaces):
+        dB = torch.empty(1, N, K, device="cuda")
+        out = [torch.empty(t.shape, dtype=BF16, device="cuda") for t in (G, H)]
+        for _ in range(3):
+            for t, o, w in zip((G, H), out, spaces[1:]):
+                moe.moe_orthogonalize(t, *t.shape, moe.MOE_GRAD_F32, 5, COEFFS, 1e-7, 1.0, o, w)
+            moe.moe_grouped_gemm_wgrad(dC, A, off, R, 1, N, K, moe.MOE_GRAD_F32, 0, dB, ws=spaces[0])
+        return [dB, *out]
+
+    def spaces():
+        return [_ws(1 << 23), *(_ws(moe.moe_orthogonalize_workspace_size(*t.shape)) for t in (G, H))]
+
+    want = [t.clone() for t in run(spaces())]
+    for t, ref in zip((G, H), want[1:]):
+        check_orth(ref, newton64(t, 5), 5)
+    two, streams, got = [spaces(), spaces()], [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, sp in zip(streams, two):
+            with torch.cuda.stream(s):
+                got.append(run(sp))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.append(run(two[0]))
+    for _ in range(2):
+        for t in got[-1]:
+            t.fill_(7)
+        graph.replay()
+    torch.cuda.synchronize()
+    for outs in got:
+        for t, w in zip(outs, want):
+            assert torch.equal(t, w)
+    assert all(moe.moe_get_device_status(w) == 0 for sp in two for w in sp)
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 @pytest.mark.parametrize("shape", [(2, 96, 200), (2, 200, 96)])
 def test_orthogonalize_steps_and_scale(shape, steps):
