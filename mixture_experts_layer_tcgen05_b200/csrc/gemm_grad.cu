@@ -143,7 +143,8 @@ struct RowGrad {
     return Warp::at64(box, lane / 2 + p / 2 * 16, (lane & 1) * 2 + p % 2);
   }
   static __device__ __forceinline__ uint4 pack8(const float* v) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
   }
   static __device__ __forceinline__ void put_half(uint32_t box, int lane, const float (&v)[32]) {
 #pragma unroll
@@ -166,7 +167,8 @@ struct RowGrad {
       if (p) __syncwarp();
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(Warp::at128(box, r, lane >> 2) + (lane & 3) * 4), "f"(v[16 * p + r])
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(Warp::at128(box, r, lane >> 2) + (lane & 3) * 4),
+                     "f"(v[16 * p + r])
                      : "memory");
       __syncwarp();
 #pragma unroll

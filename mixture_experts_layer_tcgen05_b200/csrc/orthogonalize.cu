@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
 // Tiles are 256 x 256 of a pair of SMs, or 128 x 128 of one where those are at
 // most two for each SM in the largest product (a X + B X): then more SMs, an
 // epilogue of half the columns and no pair to set up shorten each launch
-// (measured: eight 512 x 128 96 us, 127 with pairs; 7168 x 256 141 and 178; four
-// 2048 x 512 178 and 200; two 2048 x 2048, 512 such tiles, 519 and 381).
+// (measured: 7168 x 256 141 us, 178 with pairs; four 2048 x 512 178 and 200; two
+// 2048 x 2048, 512 such tiles, 519 and 381).
 constexpr int kSms = 148;
 inline bool small_tiles(int64_t nb, int64_t mp, int64_t np) {
   return nb * ceil_div(mp, 128) * ceil_div(np, 128) <= 2 * kSms;
@@ -517,8 +517,9 @@ inline int64_t square_tiles(int64_t pp, int64_t side) { return ceil_div(pp, side
 // Parts that A's sum is cut into: as many as give every SM (pair) a tile, of at
 // least four k blocks each and no more than the parts' buffer (at most as large
 // as the stack in fp32) holds; none for sums below 16 k blocks, which the launch
-// that adds the parts would not pay for (measured: one 512 x 128 134 us in parts,
-// 129 without; 1024 x 128 133 and 139; 2048 x 256 158 and 182).
+// that adds the parts would not pay for (measured: 8 k blocks, one 512 x 128
+// before it had a form of its own, 134 us in parts, 129 without; 16 k blocks, 1024 x
+// 128, 133 and 139; 2048 x 256 158 and 182).
 inline int64_t units_of(int64_t pp, int64_t side) { return kSms / (side / 128) / square_tiles(pp, side); }
 inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
   const int64_t nkb = std::max(mp, np) / BK;

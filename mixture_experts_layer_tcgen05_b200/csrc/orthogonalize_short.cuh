@@ -63,6 +63,7 @@ __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
 template <int C>
 __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   extern __shared__ uint8_t raw[];
@@ -183,7 +184,10 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
 #pragma unroll
     for (int r = 0; r < C; ++r) {
       double v;
-      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(ptx::map_to_cta(ptx::smem_addr(&norm_of), r)) : "memory");
+      asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                   : "=d"(v)
+                   : "r"(ptx::map_to_cta(ptx::smem_addr(&norm_of), r))
+                   : "memory");
       sum += v;
     }
   }
@@ -270,9 +274,9 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       const int others = (o.p + o.own - 1) / o.own - adds;
       if (others) ptx::mbar_arrive_expect_tx(bar + 24, others * o.own * 256);
     }
-    if (C > 1 && warp == 0 && lane < C && lane != rank && lane * o.own < o.p)
-      ptx::bulk_copy_to_cta(ptx::map_to_cta(got_at + rank * o.own * 512, lane), part_at + lane * o.own * 512, o.own * 512,
-                            ptx::map_to_cta(bar + 16, lane));
+    if (C > 1 && ok && warp == 0 && lane < C && lane != rank && lane * o.own < o.p)
+      ptx::bulk_copy_to_cta(ptx::map_to_cta(got_at + rank * o.own * 512, lane), part_at + lane * o.own * 512,
+                            o.own * 512, ptx::map_to_cta(bar + 16, lane));
     __syncwarp();
     if (adds) {
       if (C > 1) wait(2);
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     }
     if constexpr (C > 1) {
       hand_over();
-      if (adds && warp < 2 && lane < C && lane != rank) {  // a warp for each of A's blocks of 64 columns
+      if (adds && ok && warp < 2 && lane < C && lane != rank) {  // a warp for each of A's blocks of 64 columns
         const uint32_t from = a_at + warp * 16384 + mine * 128;
         ptx::bulk_copy_to_cta(ptx::map_to_cta(from, lane), from, o.own * 128, ptx::map_to_cta(bar + 24, lane));
       }
@@ -384,7 +388,8 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
             for (int u = 0; u < 4; ++u)
               if (col + 8 * u < o.q)
                 *reinterpret_cast<uint4*>(dst + 8 * u) =
-                    make_uint4(pack_bf16x2(f * v[8 * u], f * v[8 * u + 1]), pack_bf16x2(f * v[8 * u + 2], f * v[8 * u + 3]),
+                    make_uint4(pack_bf16x2(f * v[8 * u], f * v[8 * u + 1]),
+                               pack_bf16x2(f * v[8 * u + 2], f * v[8 * u + 3]),
                                pack_bf16x2(f * v[8 * u + 4], f * v[8 * u + 5]),
                                pack_bf16x2(f * v[8 * u + 6], f * v[8 * u + 7]));
           } else {
@@ -402,7 +407,9 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       }
     }
   }
-  // the others have what was sent to them
+  // the others have what was sent to them (a wait that gave up: time for what is still on its way)
+  if (!ok)
+    for (int i = 0; i < 100; ++i) __nanosleep(1000);
   ptx::tc_fence_before();
   __syncwarp();
   if constexpr (C > 1) ptx::cluster_sync();
