@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
   const int b = (int)blockIdx.y, r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
   const int64_t one = (int64_t)pp * pp, at = b * one + (int64_t)(r0 + r) * pp + c0 + c;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int p = 0; p < parts; ++p) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(part + (int64_t)p * nb * one + at));
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
@@ -515,7 +515,7 @@ inline bool small_tiles(int64_t nb, int64_t mp, int64_t np) {
 inline int64_t square_tiles(int64_t pp, int64_t side) { return ceil_div(pp, side) * (ceil_div(pp, side) + 1) / 2; }
 
 // Parts that A's sum is cut into: as many as give every SM (pair) a tile, of at
-// least four k blocks each and no more than the parts' buffer (at most as large
+// least eight k blocks each (7168 x 256: 128 us in 14 parts, 136 in 28) and no more than the parts' buffer (at most as large
 // as the stack in fp32) holds; none for sums below 16 k blocks, which the launch
 // that adds the parts would not pay for (measured: 8 k blocks, one 512 x 128
 // before it had a form of its own, 134 us in parts, 129 without; 16 k blocks, 1024 x
@@ -525,7 +525,7 @@ inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
   const int64_t nkb = std::max(mp, np) / BK;
   if (nkb < 16) return 1;
   const int64_t units = small_tiles(nb, mp, np) ? units_of(pp, 128) : units_of(pp, 256);
-  return std::max<int64_t>(1, std::min({units / nb, nkb / 4, mp * np / (pp * pp)}));
+  return std::max<int64_t>(1, std::min({units / nb, nkb / 8, mp * np / (pp * pp)}));
 }
 
 // Narrow matrices, p <= 8: every step in one launch and in fp32 on the FMA
@@ -784,7 +784,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
     if (p <= 4) return sized(std::integral_constant<int, 4>{});
     return sized(std::integral_constant<int, 8>{});
   }
-  if (is_short(rows, cols)) {
+  if (is_short(stack, rows, cols)) {
     ShortArgs args;
     args.g = g;
     args.out = st.out;
@@ -808,7 +808,8 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       case 1: return launch_short<1>(args, nb, s);
       case 2: return launch_short<2>(args, nb, s);
       case 4: return launch_short<4>(args, nb, s);
-      default: return launch_short<8>(args, nb, s);
+      case 8: return launch_short<8>(args, nb, s);
+      default: return launch_short<16>(args, nb, s);
     }
   }
   const dim3 ngrid((unsigned)P.chunks, (unsigned)nb);

@@ -24,8 +24,7 @@
 // 512 x 128 43 and 84 us, one 128 x 128 28 and 74, 16 x 512 25 and 67, 100 x 2000 57
 // and 95, a thousand 128 x 128 199 and 648, 64 of 2048 x 128 316 and 339. A CTA's
 // slice is at most the 256 columns that shared memory has room for beside the parts of
-// A (at 512 columns and with the loads of the others' memory, one 128 x 4096 was no
-// faster than the general form), so longer sides than 8 x 256 are the general form's.
+// A; the rest is the general form's.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -36,6 +35,7 @@ namespace moe {
 namespace mm {
 
 constexpr int kShort = 128, kShortSlice = 256, kShortThreads = 256, kShortMost = 8;  // p, columns of a CTA, CTAs
+// of a cluster that every device grants
 // X, A, the part of A (which B replaces), and the parts that others sent
 constexpr size_t kShortSmem = 1024 + kShortSlice * 256 + 32768 + 2 * 65536;
 constexpr int kShortLow = 256;  // TMEM: two accumulators of 128 columns, then the lower halves
@@ -418,6 +418,42 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
+template <int C>
+static cudaError_t size_short() {
+  static std::atomic<uint64_t> sized{0};
+  if (C > kShortMost) {
+    cudaError_t e = cudaFuncSetAttribute(short_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return set_smem_once(sized, short_kernel<C>, kShortSmem);
+}
+
+// How many clusters of 16, a size that a device need not grant, the current one
+// runs at a time.
+static int clusters_of_16() {
+  static std::atomic<int> known[64];  // that number and 1
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kShortThreads);
+  cfg.dynamicSmemBytes = kShortSmem;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 16;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (size_short<16>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, short_kernel<16>, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // not this call's error
+    n = 0;
+  }
+  if (dev < 64) known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 // The fewest CTAs that hold a matrix; more, down to slices of 128 columns, while
 // they all find an SM (eight 512 x 128: 47 us with slices of 128 or 64, 62 with 256).
 inline int short_cluster(int64_t stack, int64_t q) {
@@ -426,14 +462,18 @@ inline int short_cluster(int64_t stack, int64_t q) {
   while (c < kShortMost && c * 128 < q && stack * c * 2 <= kSms) c *= 2;
   return c;
 }
-inline bool is_short(int64_t rows, int64_t cols) {
-  return std::min(rows, cols) <= kShort && std::max(rows, cols) <= kShortSlice * kShortMost;
+// Sides past eight slices take clusters of 16, of which few run at a time: only
+// stacks that run at once (128 x 4096: one 65 us, 100 in the general form; 16 of them
+// 192 and 240, but 64 of 64 x 4096 565 and 381, 128 of 128 x 2500 1989 and 808).
+inline bool is_short(int64_t stack, int64_t rows, int64_t cols) {
+  const int64_t q = std::max(rows, cols);
+  return std::min(rows, cols) <= kShort &&
+         (q <= kShortSlice * kShortMost || (q <= kShortSlice * 16 && stack <= clusters_of_16()));
 }
 
 template <int C>
 static cudaError_t launch_short(const ShortArgs& args, int nb, cudaStream_t s) {
-  static std::atomic<uint64_t> sized{0};
-  cudaError_t e = set_smem_once(sized, short_kernel<C>, kShortSmem);
+  cudaError_t e = size_short<C>();
   if (e != cudaSuccess) return e;
   return launch_overlapped_smem(short_kernel<C>, dim3((unsigned)(nb * C)), kShortThreads, kShortSmem, s, C, args);
 }

@@ -481,7 +481,8 @@ def test_orthogonalize(nb, rows, cols, dtype):
 @pytest.mark.parametrize("tall", [False, True])
 @pytest.mark.parametrize("nb,p,q", [(2, 9, 9), (1, 16, 64), (1, 31, 65), (1, 32, 511), (2, 33, 128), (1, 34, 1000),
                                     (1, 60, 61), (2, 64, 513), (1, 65, 1025), (1, 72, 192), (3, 97, 97), (1, 104, 1536),
-                                    (1, 127, 2047), (1, 128, 2048), (1, 128, 2049), (1, 129, 512), (40, 20, 300),
+                                    (1, 127, 2047), (1, 128, 2048), (1, 128, 2049), (2, 10, 3000), (1, 128, 4096),
+                                    (1, 77, 4097), (10, 64, 2500), (1, 129, 512), (40, 20, 300),
                                     (30, 128, 700), (160, 24, 257), (20, 100, 2000)])
 def test_orthogonalize_short_sides(nb, p, q, tall):
     """Every size of cluster, rows that end inside a warp's or a CTA's share, slices that end past the matrix."""
