@@ -307,6 +307,10 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       }
       __syncwarp();
       if ((o.p + o.own - 1) / o.own > adds) wait(3);
+      if (step == o.steps - 1) {  // all that was sent to this CTA has come
+        __syncwarp();
+        ptx::cluster_arrive_relaxed();
+      }
     }
     hand_over();
     if (tid == 0) issue_square(a_at, ksteps);
@@ -407,13 +411,12 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       }
     }
   }
-  // the others have what was sent to them (a wait that gave up: time for what is still on its way)
+  // a wait that gave up: time for what is still on its way here
   if (!ok)
     for (int i = 0; i < 100; ++i) __nanosleep(1000);
   ptx::tc_fence_before();
-  __syncwarp();
-  if constexpr (C > 1) ptx::cluster_sync();
-  else __syncthreads();
+  __syncthreads();
+  if constexpr (C > 1) ptx::cluster_wait();  // the others have what this CTA sent
   ptx::tc_fence_after();
   if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
