@@ -19,7 +19,7 @@
 //     X <- a X + B X in place: a chunk's MMAs read that chunk's columns alone.
 // Bound by latency. Of a step's 12700 cycles (128 x 128 to a CTA, four CTAs) the
 // issue of the 24 MMAs takes 2500, the exchange of A 6200 (a third of it the copies'
-// bytes, 48 KB each way) and the epilogues 3700; before the first step 13000 go to
+// bytes, 48 KB each way) and the epilogues 3700; before the first step 10000 go to
 // reading G and its norm. Measured, against the launches of the general form: eight
 // 512 x 128 43 and 84 us, one 128 x 128 28 and 74, 16 x 512 25 and 67, 100 x 2000 57
 // and 95, a thousand 128 x 128 199 and 648, 64 of 2048 x 128 316 and 339. A CTA's
