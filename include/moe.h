@@ -391,7 +391,7 @@ typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
  *   gated (SWIGLU, GEGLU, REGLU): d is the gradient of h = act(g) * u, and
  *           dA[m, k] = d u act'(g) (gradient of g), dA[m, K + k] = d act(g)
  *           (gradient of u), h[m, k] = act(g) u (recomputed, for the weight
- *           gradient of the down projection). relu'(0) = 0.
+ *           gradient of the down projection). relu'(0) = 0; a NaN gate makes all three NaN.
  *   dC_dev bf16 [M_total, N]
  *   B_dev  bf16 [E, N, K], the weights that the forward product reads
  *   gu_dev bf16 [M_total, 2K] (gated: g, then u, per row), else NULL

@@ -17,7 +17,7 @@ namespace mm {
 // The gate's activation a(g) and its derivative.
 //   silu: p = 1 / (1 + e^-g), a = g p, a' = p (1 + g (1 - p))
 //   gelu: a = g Phi(g), a' = Phi(g) + g phi(g)
-//   relu: a = max(g, 0), a' = [g > 0]
+//   relu: a = max(g, 0), a' = [g > 0]; both NaN where g is
 template <int ACT>
 __device__ __forceinline__ void act_grad(float g, float& a, float& da) {
   if constexpr (ACT == kActSilu) {
@@ -30,8 +30,9 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& da) {
     a = g * p;
     da = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
   } else {
-    a = fmaxf(g, 0.0f);
-    da = g > 0.0f ? 1.0f : 0.0f;
+    // (fmaxf would give 0 for a NaN, which the step would train on unseen)
+    a = g > 0.0f || g != g ? g : 0.0f;
+    da = g > 0.0f ? 1.0f : g != g ? g : 0.0f;
   }
 }
 
