@@ -4,6 +4,8 @@ import math
 
 import pytest
 
+from helpers import Guarded
+
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +82,75 @@ def test_gates_that_are_no_numbers(R, N, room, act):
     same = torch.ones_like(real)
     same[[1, R - 1]] = False
     assert torch.equal(got[same], clean[same])
+
+
+# ----------------------------------------------- updates of large stacks
+COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def newton64(G, steps, coeffs=COEFFS, eps=1e-7, scale=1.0):
+    a, b, c = coeffs
+    out = []
+    for g in G.double():
+        x = g / (g.norm() + eps)
+        for _ in range(steps):
+            if x.shape[0] <= x.shape[1]:
+                s = x @ x.T
+                x = a * x + (b * s + c * s @ s) @ x
+            else:
+                s = x.T @ x
+                x = a * x + x @ (b * s + c * s @ s)
+        out.append(x * scale)
+    return torch.stack(out)
+
+
+def orth(G, steps=5, coeffs=COEFFS, eps=1e-7, scale=1.0, hold=None):
+    """hold: matrices that the workspace has room for."""
+    nb, m, n = G.shape
+    out = Guarded((nb, m, n), BF16, fill=0x7B)
+    ws = Guarded((moe.moe_orthogonalize_workspace_size(hold or nb, m, n),), torch.uint8, fill=0xFF)
+    ws.t[:256] = 0
+    moe.moe_orthogonalize(G, nb, m, n, moe.MOE_GRAD_F32 if G.dtype == torch.float32 else moe.MOE_GRAD_BF16, steps,
+                          coeffs, eps, scale, out.t, ws.t)
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(ws.t) == 0 and out.intact() and ws.intact()
+    return out.t
+
+
+def errors(got, ref):
+    """Each matrix's distance from the reference, of the reference's norm."""
+    assert torch.isfinite(got).all()
+    return ((got.double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)).max().item()
+
+
+def orth_tol(steps):
+    """Three operands a step are rounded to fp16, the result to bf16."""
+    return 2.0**-8 + steps * 3 * 2.0**-11
+
+
+# more than 296 tiles of 128 x 128: tiles of pairs of SMs; A's sum whole, and (one matrix) in parts
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("shape", [(20, 520, 1000), (20, 1000, 520), (6, 700, 2001), (6, 2001, 700), (5, 1500, 1500),
+                                   (40, 260, 1028), (40, 1028, 260), (7, 3100, 260), (1, 300, 30000), (1, 30001, 257),
+                                   (2, 513, 12000)])
+def test_orthogonalize_large_stacks(shape, dtype):
+    G = _randn(_gen(sum(shape)), *shape, dtype=dtype)
+    ref = newton64(G, 5)
+    err = errors(orth(G), ref)
+    assert err <= orth_tol(5), err
+    if shape[0] > 1:
+        err = errors(orth(G, hold=max(1, shape[0] // 3)), ref)
+        assert err <= orth_tol(5), err
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3])
+@pytest.mark.parametrize("shape", [(20, 520, 1000), (20, 1000, 520), (6, 700, 2001), (6, 2001, 700)])
+def test_orthogonalize_large_stacks_steps_and_rank(shape, steps):
+    nb, m, n = shape
+    G = _randn(_gen(steps), *shape, dtype=torch.float32, std=1e-3)
+    err = errors(orth(G, steps=steps, scale=-0.25), newton64(G, steps, scale=-0.25))
+    assert err <= orth_tol(steps), err
+    gen = _gen(steps + 50)
+    G = _randn(gen, nb, m, 4 * steps, dtype=torch.float32) @ _randn(gen, nb, 4 * steps, n, dtype=torch.float32)
+    err = errors(orth(G), newton64(G, 5))
+    assert err <= orth_tol(5), err
