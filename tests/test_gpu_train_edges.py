@@ -4,6 +4,7 @@ import math
 
 import pytest
 
+import orth_numbers as on
 from helpers import Guarded
 
 torch = pytest.importorskip("torch")
@@ -154,3 +155,27 @@ def test_orthogonalize_large_stacks_steps_and_rank(shape, steps):
     G = _randn(gen, nb, m, 4 * steps, dtype=torch.float32) @ _randn(gen, nb, 4 * steps, n, dtype=torch.float32)
     err = errors(orth(G), newton64(G, 5))
     assert err <= orth_tol(5), err
+
+
+# ------------------------------------------------ the numbers of an update
+@pytest.mark.parametrize("rank", [None, 4])
+@pytest.mark.parametrize("shape", on.SHAPES)
+def test_orthogonalize_is_as_exact_as_its_roundings(shape, rank):
+    """No further from the formula than its own roundings, done on the CPU; alone, and in a stack of large tiles."""
+    G = on.matrix(shape, rank)
+    ref = on.newton64(G, 5)
+    tol = on.MARGIN * on.distance(on.rounded(G, 5), ref)
+    for nb in (1, 60):
+        out = orth(G.cuda().expand(nb, *shape).contiguous()).cpu()
+        err = on.distance(out[0], ref)
+        assert err <= tol, (nb, err, tol)
+        assert torch.equal(out, out[:1].expand(nb, *shape))
+
+
+@pytest.mark.parametrize("nb,rows,cols", [(1, 4, 7), (3, 7, 4), (1, 16, 16), (2, 16, 700), (2, 700, 16), (1, 64, 2048),
+                                          (1, 4000, 64), (1, 256, 256), (1, 300, 256), (1, 256, 2000),
+                                          (80, 256, 300), (80, 300, 256)])
+def test_orthogonalize_gives_the_diagonals_rest_back(nb, rows, cols):
+    coeffs, value = on.diagonal_case(min(rows, cols))
+    G = torch.eye(rows, cols, device="cuda").expand(nb, rows, cols).contiguous()
+    assert torch.equal(orth(G, steps=1, coeffs=coeffs, eps=0.0), (G * value).to(BF16))
