@@ -452,7 +452,7 @@ moe_status_t moe_combine_backward(const void* dout_dev, const void* y_perm_dev, 
  *           use). Calls that may run at the same time, captured graphs included,
  *           need a workspace each.
  * Any rows and cols in [1, 2^20], nb * (rows + 63) < 2^31. The state X is held in
- * two fp16 halves (22 bits); the products take the upper half (scaled so that
+ * two fp16 halves (22 bits, of a multiple near 1 where eps makes X small); the products take the upper half (scaled so that
  * |X|_2 about 1, which the norm and a polynomial with bounded steps give, fits)
  * and accumulate in fp32; matrices with at most 8 rows or columns are computed in
  * fp32. A polynomial that lets |X|_2 grow past some hundreds gives Inf or NaN. A

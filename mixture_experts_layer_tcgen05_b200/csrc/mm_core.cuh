@@ -161,6 +161,7 @@ struct Warp {
   uint32_t parity;   // bit i: parity of barrier i's next phase
   uint32_t pending;  // bit i: a load is in flight on barrier i
   int32_t* status;
+  float4 own;        // the Op's own, from prefetch to epilogue
 
   // first row of this warp in a tile that starts at row m
   __device__ __forceinline__ int row0(int m) const { return m + rank * BM + q * 32; }
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     Warp w{&maps, rank, q, half, lane, ptx::smem_addr(stage_out) + (warp - 4) * Op::kStageWarp,
-           load0 + (warp - 4) * 16, 0, 0, status};
+           load0 + (warp - 4) * 16, 0, 0, status, {}};
     int acc = 0;
     uint32_t acc_ph = 0;
     bool ok = true;

@@ -23,10 +23,13 @@
 // result's norm over spectra from white to rank 4 (bf16 operands: 3e-3 to
 // 1.4e-2), at the same MMA rate. The largest part of that is the diagonal of
 // b A + c A^2, which nears b + c while the rest of it nears 0: what its rounding
-// takes is kept in fp32 and given back as a factor of X (a fifth to a third less). fp16's range holds because everything is stored
-// times s = 2^floor(log2(q) / 2): |X|_2 and |A|_2 stay near 1, so entries of X
-// reach from 1 / sqrt(p q) to 1, and those of A from 1 / (p sqrt(q)) to 1. The
-// norm is summed in fp64.
+// takes is kept in fp32 and given back as a factor of X (a fifth to a third
+// less). fp16's range holds because everything is stored times s = 2^floor(log2(q)
+// / 2): |X|_2 and |A|_2 stay near 1, so entries of X reach from 1 / sqrt(p q) to 1,
+// and those of A from 1 / (p sqrt(q)) to 1. Where eps is not small beside |G|_F, X
+// starts below that, at rho = |G|_F / (|G|_F + eps) (an expert without rows has a
+// momentum that decays past any eps); then 2^-t X is stored, which is near 1, and
+// takes b 4^t and c 16^t (step_factors). The norm is summed in fp64.
 //
 // Three forms: p <= 8 on the FMA units (narrow_kernel), p <= 128 in one launch
 // (orthogonalize_short.cuh), and this file's launches over MMA tiles.
@@ -51,9 +54,11 @@ struct Stack {
   int nb, rows, cols;    // the caller's matrices
   int mp, np, pp;        // padded rows, cols and min(rows, cols)
   float s, inv_s;        // the operands' scale and its inverse
-  float a, b, c, scale;
+  float a;
   const void* g;         // [nb, rows, cols] fp32 or bf16
-  const float2* inv;     // [nb] 1 / (|G|_F + eps) as a power of two and the rest
+  const float2* inv;     // [nb] 2^-t / (|G|_F + eps) as a power of two and the rest
+  const float4* factors; // [nb, steps] of each step (step_factors)
+  int step, steps;
   float* rest;           // [nb, pp] what rounding took from the diagonal of b A + c A^2
   __nv_bfloat16* out;    // [nb, rows, cols]
   bool from_g, last;     // the step reads G as its state; it is the last one
@@ -131,12 +136,15 @@ struct Square {
            w.row0(t.p[1]), t.p[0], 2048);
   }
   __device__ void prefetch(const Tile& t, Warp& w) const {
-    if (POLY && steps(t, w) > 0) load_gram(t, w, 0);
+    if (!POLY || steps(t, w) == 0) return;
+    load_gram(t, w, 0);
+    w.own = st.factors[(int64_t)t.p[0] * st.steps + st.step];
   }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
     const int row0 = w.row0(t.p[1]), n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
     const bool mirror = t.p[1] != t.p[2];  // a tile on the diagonal holds both halves itself
-    const float ci = st.c * st.inv_s;
+    const float4 f = w.own;
+    const float ci = f.y * st.inv_s;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int col = col0 + 32 * i;
@@ -151,9 +159,9 @@ struct Square {
           const uint32_t p[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
-            v[8 * u + 2 * j] = fmaf(st.b, f.x, ci * v[8 * u + 2 * j]);
-            v[8 * u + 2 * j + 1] = fmaf(st.b, f.y, ci * v[8 * u + 2 * j + 1]);
+            const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
+            v[8 * u + 2 * j] = fmaf(f.x, e.x, ci * v[8 * u + 2 * j]);
+            v[8 * u + 2 * j + 1] = fmaf(f.x, e.y, ci * v[8 * u + 2 * j + 1]);
           }
         }
       } else if constexpr (MODE == kPart) {
@@ -259,14 +267,18 @@ struct Apply {
     if (steps(t, w) == 0) return;
     w.free_boxes();
     load_state(t, w, 0);
+    w.own = st.factors[(int64_t)t.p[0] * st.steps + st.step];
   }
   __device__ bool epilogue(const Tile& t, Warp& w, uint32_t taddr) const {
     const int row0 = w.row0(t.p[1]), row = row0 + w.lane, n = steps(t, w), col0 = t.p[2] + w.half * (kBN / 2);
-    // v = s (a X + B X): the accumulator holds s^2 B X, but for the rest of B's
-    // diagonal, which joins a: one of this row (LEFT), or one of each column
+    // v = s (a X + B X), times the step's change of t: the accumulator holds s^2 B X,
+    // but for the rest of B's diagonal, which joins a: one of this row (LEFT), or one
+    // of each column
+    const float4 f = w.own;
+    const float inv_s = f.z * st.inv_s;
     const float2 inv = st.from_g ? st.inv[t.p[0]] : make_float2(1.0f, 1.0f);
     const float* rest = st.rest + (int64_t)t.p[0] * st.pp;
-    const float a_row = LEFT && row < st.pp ? st.a + rest[row] : st.a;
+    const float a_row = f.z * (LEFT && row < st.pp ? st.a + rest[row] : st.a);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int col = col0 + 32 * i;
@@ -277,12 +289,12 @@ struct Apply {
       load_acc32(taddr + w.half * (kBN / 2) + 32 * i, v);
       if (!w.wait(i & 1)) return false;
       if (st.from_g) {
-        const float f = st.s * inv.y;
+        const float y = st.s * inv.y;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint4 g = Warp::get(Warp::at128(box, w.lane, j));
-          x[4 * j] = inv.x * __uint_as_float(g.x) * f, x[4 * j + 1] = inv.x * __uint_as_float(g.y) * f;
-          x[4 * j + 2] = inv.x * __uint_as_float(g.z) * f, x[4 * j + 3] = inv.x * __uint_as_float(g.w) * f;
+          x[4 * j] = inv.x * __uint_as_float(g.x) * y, x[4 * j + 1] = inv.x * __uint_as_float(g.y) * y;
+          x[4 * j + 2] = inv.x * __uint_as_float(g.z) * y, x[4 * j + 3] = inv.x * __uint_as_float(g.w) * y;
         }
         __syncwarp();  // every lane has its row of G: the box may take the halves
       } else {
@@ -302,15 +314,15 @@ struct Apply {
         float4 d = make_float4(a_row, a_row, a_row, a_row);
         if constexpr (!LEFT) {
           const float4 r = __ldg(reinterpret_cast<const float4*>(rest + col) + j);
-          d.x += r.x, d.y += r.y, d.z += r.z, d.w += r.w;
+          d = make_float4(f.z * (st.a + r.x), f.z * (st.a + r.y), f.z * (st.a + r.z), f.z * (st.a + r.w));
         }
-        v[4 * j] = fmaf(d.x, x[4 * j], st.inv_s * v[4 * j]);
-        v[4 * j + 1] = fmaf(d.y, x[4 * j + 1], st.inv_s * v[4 * j + 1]);
-        v[4 * j + 2] = fmaf(d.z, x[4 * j + 2], st.inv_s * v[4 * j + 2]);
-        v[4 * j + 3] = fmaf(d.w, x[4 * j + 3], st.inv_s * v[4 * j + 3]);
+        v[4 * j] = fmaf(d.x, x[4 * j], inv_s * v[4 * j]);
+        v[4 * j + 1] = fmaf(d.y, x[4 * j + 1], inv_s * v[4 * j + 1]);
+        v[4 * j + 2] = fmaf(d.z, x[4 * j + 2], inv_s * v[4 * j + 2]);
+        v[4 * j + 3] = fmaf(d.w, x[4 * j + 3], inv_s * v[4 * j + 3]);
       }
       if (st.last) {
-        const float r = st.scale * st.inv_s;
+        const float r = f.w * st.inv_s;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t o[4];
@@ -371,13 +383,51 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-// 1 / (|G|_F + eps), from the sum of squares, as x y, x a power of two near 1 /
-// |G|_F: the norm of entries near fp32's largest has an inverse below fp32's
-// smallest normal.
-__device__ __forceinline__ float2 inverse_norm(double sum, float eps) {
+// 1 / (|G|_F + eps), from the sum of squares, as x y 2^t. x is a power of two near 1
+// / |G|_F: the norm of entries near fp32's largest has an inverse below fp32's
+// smallest normal. rho = |G|_F / (|G|_F + eps), and 2^-t rho is in [1/2, 1]; t is
+// 0 where that is so without it, and where rho is 0 or NaN.
+struct Unit {
+  float x, y;
+  int t;
+  double rho;
+};
+__device__ __forceinline__ Unit unit_norm(double sum, float eps) {
   const double norm = sqrt(sum);
   const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
-  return make_float2((float)p2, (float)(1.0 / (norm * p2 + (double)eps * p2)));
+  const double y = 1.0 / (norm * p2 + (double)eps * p2);
+  Unit u = {(float)p2, (float)y, 0, norm * p2 * y};
+  if (u.rho > 0.0 && u.rho < 0.5) {
+    u.t = ilogb(u.rho) + 1;
+    u.y = (float)ldexp(y, -u.t);
+  }
+  return u;
+}
+
+constexpr int kMostSteps = 64;  // (of a call, as the entry checks)
+
+// The factors of every step of a matrix that is stored as 2^-t X (and whose A is, so,
+// as 4^-t A): b 4^t, c 16^t, 2^(t - t') for the t' of the next step, and scale 2^t,
+// which the last one's result takes. t follows a bound of |X|_F up to 0 and no
+// further: |X'| <= |a| |X| + |b| |X|^3 + |c| |X|^5. What fp16 loses of a small b A + c
+// A^2 is below 2^-25 of X, beside a X. By the block's threads, `put` in any order.
+template <class F>
+__device__ __forceinline__ void step_factors(const Unit& u, float a, float b, float c, float scale, int steps, F put) {
+  if (u.t == 0) {  // most matrices: t stays there
+    for (int i = threadIdx.x; i < steps; i += blockDim.x) put(i, make_float4(b, c, 1.0f, scale));
+    return;
+  }
+  if (threadIdx.x != 0) return;
+  int t = u.t;
+  double bound = u.rho;
+  for (int i = 0; i < steps; ++i) {
+    const double x2 = bound * bound;
+    bound *= fabs((double)a) + x2 * (fabs((double)b) + x2 * fabs((double)c));
+    const int next = i == steps - 1 ? t : bound < 0.5 ? max(t, ilogb(bound) + 1) : 0;
+    put(i, make_float4((float)ldexp((double)b, 2 * t), (float)ldexp((double)c, 4 * t), (float)ldexp(1.0, t - next),
+                       (float)ldexp((double)scale, t)));
+    t = next;
+  }
 }
 
 // part[b][chunk] = the sum of squares of a chunk of matrix b, in fp64 (squares
@@ -408,20 +458,27 @@ __global__ void __launch_bounds__(kNormThreads) sumsq_kernel(const T* __restrict
   if (threadIdx.x == 0) part[b * chunks + blockIdx.x] = s;
 }
 
-// The upper half of s G / (|G|_F + eps), zero in the padding; inv[b] kept for a
-// first step that reads G as its state, else (xl given) the lower half too.
+// The upper half of s 2^-t G / (|G|_F + eps), zero in the padding; inv[b] kept for a
+// first step that reads G as its state, else (xl given) the lower half too; and the
+// steps' factors.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(Stack st, const double* __restrict__ part,
-                                                                 int chunks, float eps, float2* __restrict__ inv,
+                                                                 int chunks, float b_coeff, float c_coeff, float scale,
+                                                                 float eps, float2* __restrict__ inv,
+                                                                 float4* __restrict__ factors,
                                                                  __half* __restrict__ xh, __half* __restrict__ xl) {
   ptx::let_next_grid_start();
   ptx::wait_for_previous_grid();
   const int64_t b = blockIdx.y;
   double v = 0.0;
   for (int i = threadIdx.x; i < chunks; i += kNormThreads) v += part[b * chunks + i];
-  const float2 f = inverse_norm(block_sum(v), eps);
+  const Unit f = unit_norm(block_sum(v), eps);
   const float p = f.x, r = f.y;
-  if (blockIdx.x == 0 && threadIdx.x == 0) inv[b] = make_float2(p, r);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) inv[b] = make_float2(p, r);
+    step_factors(f, st.a, b_coeff, c_coeff, scale, st.steps,
+                 [&](int i, float4 v) { factors[b * st.steps + i] = v; });
+  }
   const T* src = static_cast<const T*>(st.g) + b * st.rows * st.cols;
   const int64_t base = b * st.mp * st.np;
   // odd rows: a warp takes 64 columns of a row at a time, lane = column (with the
@@ -610,8 +667,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   sync();
   s = 0.0;
   for (int r = 0; r < CLUSTER; ++r) s += CLUSTER > 1 ? peer_f64(&norm_of, r) : norm_of;
-  const float2 factors = inverse_norm(s, eps);
-  const float f = factors.x, inv = factors.y;
+  const Unit unit = unit_norm(s, eps);
+  const float f = unit.x, inv = ldexpf(unit.y, unit.t);  // (fp32 has room for a small X)
 
   // step -1 takes G; step i < steps - 1 leaves A of the one after it
 #pragma unroll 1
@@ -697,7 +754,7 @@ namespace mm {
 
 struct OrthPlan {
   int64_t mp, np, pp, chunks;
-  int64_t part, inv, rest, xl, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
+  int64_t part, inv, factors, rest, xl, xh0, xh1, gram, poly, sums, total;  // byte offsets in the workspace
 };
 
 inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
@@ -714,6 +771,7 @@ inline OrthPlan orth_plan(int64_t nb, int64_t rows, int64_t cols) {
   };
   p.part = take(nb * p.chunks * 8);
   p.inv = take(nb * 8);
+  p.factors = take(nb * kMostSteps * 16);
   p.rest = take(nb * p.pp * 4);
   p.xl = take(nb * p.mp * p.np * 2);
   p.xh0 = take(nb * p.mp * p.np * 2);
@@ -749,9 +807,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   st.s = std::ldexp(1.0f, (int)std::floor(std::log2((double)std::max(rows, cols)) / 2));
   st.inv_s = 1.0f / st.s;
   st.a = a;
-  st.b = b;
-  st.c = c;
-  st.scale = scale;
+  st.steps = steps;
   st.g = g;
   st.vec = cols % 8 == 0;
   st.out = static_cast<__nv_bfloat16*>(out);
@@ -760,6 +816,8 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
   void* poly = ws + P.poly;
   float2* inv = reinterpret_cast<float2*>(ws + P.inv);
   st.inv = inv;
+  float4* factors = reinterpret_cast<float4*>(ws + P.factors);
+  st.factors = factors;
   st.rest = reinterpret_cast<float*>(ws + P.rest);
   double* part = reinterpret_cast<double*>(ws + P.part);
   __half* xh[2] = {reinterpret_cast<__half*>(ws + P.xh0), reinterpret_cast<__half*>(ws + P.xh1)};
@@ -821,8 +879,8 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
     using T = decltype(zero);
     e = launch_overlapped(sumsq_kernel<T>, ngrid, kNormThreads, s, 1, static_cast<const T*>(g), n, (int)P.chunks, part);
     if (e == cudaSuccess)
-      e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, 1, st, (const double*)part, (int)P.chunks, eps,
-                            inv, xh[0], xl_init);
+      e = launch_overlapped(normalize_kernel<T>, cgrid, kNormThreads, s, 1, st, (const double*)part, (int)P.chunks, b, c,
+                            scale, eps, inv, factors, xh[0], xl_init);
   };
   if (g_f32) norms(0.0f);
   else norms(__nv_bfloat16());
@@ -872,6 +930,7 @@ static cudaError_t orthogonalize_batch(const void* g, int nb, int stack, int row
       const int64_t k = LEFT ? P.np : P.mp;
       st.from_g = i == 0 && g_state;
       st.last = i == steps - 1;
+      st.step = i;
       cudaError_t e = parts == 1 ? square(Square<MN, kGram, SIDE>{}, x, k, P.mp, g_io, 1)
                                  : square(Square<MN, kPart, SIDE>{}, x, k, P.mp, sums_out, parts);
       if (e == cudaSuccess && parts > 1)

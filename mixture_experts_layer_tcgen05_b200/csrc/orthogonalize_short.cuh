@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
   __shared__ uint32_t tmem_of;
   __shared__ double norm_of;
   __shared__ float rest[kShort];
+  __shared__ float4 factors[kMostSteps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = warp >> 2, row = (warp & 3) * 32 + lane;
   const int rank = C > 1 ? (int)ptx::cluster_ctarank() : 0, item = (int)blockIdx.x / C;
@@ -192,7 +193,8 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     }
   }
   {
-    const float2 inv = inverse_norm(sum, o.eps);
+    const Unit inv = unit_norm(sum, o.eps);
+    step_factors(inv, o.a, o.b, o.c, o.scale, o.steps, [&](int i, float4 v) { factors[i] = v; });
     auto init = [&](int c0, float(&v)[32]) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = inv.x * v[j] * inv.y * o.s;
@@ -247,13 +249,13 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       ptx::mma_f16(tmem + (j & 1) * 128, db + (k >> 2) * 1024 + (k & 3) * 2, dx + k * 128, i, k > 0);
     ptx::mma_commit(bar + 8 * (j & 1));
   };
-  const float ci = o.c * o.inv_s;
-
 #pragma unroll 1
   for (int step = 0; step < o.steps; ++step) {
     hand_over();
     if (tid == 0) issue_square(x_at, o.slice / 16);
     __syncwarp();
+    const float4 f = factors[step];
+    const float ci = f.y * o.inv_s, inv_s = f.z * o.inv_s;
     wait(0);
     if (used)
 #pragma unroll
@@ -328,9 +330,9 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            v[8 * u + 2 * j] = fmaf(o.b, f.x, ci * v[8 * u + 2 * j]);
-            v[8 * u + 2 * j + 1] = fmaf(o.b, f.y, ci * v[8 * u + 2 * j + 1]);
+            const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            v[8 * u + 2 * j] = fmaf(f.x, e.x, ci * v[8 * u + 2 * j]);
+            v[8 * u + 2 * j + 1] = fmaf(f.x, e.y, ci * v[8 * u + 2 * j + 1]);
           }
         }
         if (c0 == (warp & 3) * 32) {
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     }
     __syncwarp();
     const bool last = step == o.steps - 1;
-    const float a_row = o.a + rest[row];
+    const float a_row = f.z * (o.a + rest[row]);
 #pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
       wait(j & 1);
@@ -378,12 +380,12 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
             }
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = fmaf(a_row, x[k], o.inv_s * v[k]);
+          for (int k = 0; k < 32; ++k) v[k] = fmaf(a_row, x[k], inv_s * v[k]);
           if (!last) {
             put_state(c0, v);
             continue;
           }
-          const float f = o.scale * o.inv_s;
+          const float r = f.w * o.inv_s;
           const int col = first + c0;
           if (row >= o.p) continue;
           if (o.wide && o.q % 8 == 0) {
@@ -392,16 +394,16 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
             for (int u = 0; u < 4; ++u)
               if (col + 8 * u < o.q)
                 *reinterpret_cast<uint4*>(dst + 8 * u) =
-                    make_uint4(pack_bf16x2(f * v[8 * u], f * v[8 * u + 1]),
-                               pack_bf16x2(f * v[8 * u + 2], f * v[8 * u + 3]),
-                               pack_bf16x2(f * v[8 * u + 4], f * v[8 * u + 5]),
-                               pack_bf16x2(f * v[8 * u + 6], f * v[8 * u + 7]));
+                    make_uint4(pack_bf16x2(r * v[8 * u], r * v[8 * u + 1]),
+                               pack_bf16x2(r * v[8 * u + 2], r * v[8 * u + 3]),
+                               pack_bf16x2(r * v[8 * u + 4], r * v[8 * u + 5]),
+                               pack_bf16x2(r * v[8 * u + 6], r * v[8 * u + 7]));
           } else {
             __nv_bfloat16* dst = o.out + at + (o.wide ? (int64_t)row * o.q + col : (int64_t)col * o.p + row);
             const int64_t next = o.wide ? 1 : o.p;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (col + k < o.q) dst[k * next] = __float2bfloat16_rn(f * v[k]);
+              if (col + k < o.q) dst[k * next] = __float2bfloat16_rn(r * v[k]);
           }
         }
       if (j + 2 < chunks) {

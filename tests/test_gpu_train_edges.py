@@ -179,3 +179,34 @@ def test_orthogonalize_gives_the_diagonals_rest_back(nb, rows, cols):
     coeffs, value = on.diagonal_case(min(rows, cols))
     G = torch.eye(rows, cols, device="cuda").expand(nb, rows, cols).contiguous()
     assert torch.equal(orth(G, steps=1, coeffs=coeffs, eps=0.0), (G * value).to(BF16))
+
+
+# ------------------------------------------------ norms that eps is not small beside
+FORMS = [(3, 6, 500), (2, 1300, 4), (3, 40, 72), (2, 700, 100), (1, 60, 4000), (2, 130, 260), (2, 301, 190),
+         (20, 520, 700), (20, 700, 515)]  # narrow, short in clusters of 1 to 16, tiles of one SM, of pairs
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("steps", [1, 5, 12])
+@pytest.mark.parametrize("shape", FORMS)
+def test_orthogonalize_small_norms(shape, steps, dtype):
+    """X starts near |G| / eps and is as exact there; matrices of one stack each at their own size."""
+    nb, m, n = shape
+    eps = 1e-7
+    unit = _randn(_gen(m + n + steps), nb, m, n, dtype=torch.float32) / math.sqrt(m * n)
+    for norms in ([1e-7, 3e-8, 1.0], [1e-10, 1e-7, 1e-13], [1e-15, 1e-2, 1e-6], [1e-20, 1e-30, 1e-9], [2e-36, 5e-8, 1e-7]):
+        size = torch.tensor((norms * nb)[:nb], device="cuda", dtype=torch.float64)[:, None, None]
+        G = (unit.double() * size).to(dtype)
+        err = errors(orth(G, steps=steps, eps=eps), newton64(G, steps, eps=eps))
+        assert err <= orth_tol(steps), (norms, err)
+
+
+@pytest.mark.parametrize("coeffs,steps,eps", [((1.5, -0.5, 0.0), 20, 1e3), ((1.875, -1.25, 0.375), 30, 1e5),
+                                              ((3.4445, -4.7750, 2.0315), 64, 1e20), ((1.0, 0.0, 0.0), 3, 40.0),
+                                              ((-2.0, 1.0, 0.0), 9, 1e6), ((0.5, 0.25, 0.25), 4, 100.0)])
+@pytest.mark.parametrize("shape", [(2, 4, 100), (2, 40, 72), (1, 300, 130), (2, 130, 260), (20, 520, 700)])
+def test_orthogonalize_large_eps(shape, coeffs, steps, eps):
+    G = _randn(_gen(steps), *shape, dtype=torch.float32)
+    ref = newton64(G, steps, coeffs, eps)
+    err = errors(orth(G, steps=steps, coeffs=coeffs, eps=eps), ref)
+    assert err <= orth_tol(steps), err
