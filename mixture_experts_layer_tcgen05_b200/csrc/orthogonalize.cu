@@ -395,7 +395,8 @@ struct Unit {
 __device__ __forceinline__ Unit unit_norm(double sum, float eps) {
   const double norm = sqrt(sum);
   const double p2 = norm > 0.0 && isfinite(norm) ? ldexp(1.0, max(-140, min(126, -ilogb(norm)))) : 1.0;
-  const double y = 1.0 / (norm * p2 + (double)eps * p2);
+  // (a zero matrix over an eps whose inverse leaves fp32: 0, not 0 times infinity)
+  const double y = norm == 0.0 && eps > 0.0f ? 0.0 : 1.0 / (norm * p2 + (double)eps * p2);
   Unit u = {(float)p2, (float)y, 0, norm * p2 * y};
   if (u.rho > 0.0 && u.rho < 0.5) {
     u.t = ilogb(u.rho) + 1;

@@ -210,3 +210,16 @@ def test_orthogonalize_large_eps(shape, coeffs, steps, eps):
     ref = newton64(G, steps, coeffs, eps)
     err = errors(orth(G, steps=steps, coeffs=coeffs, eps=eps), ref)
     assert err <= orth_tol(steps), err
+
+
+@pytest.mark.parametrize("eps", [1e-44, 1e-40, 1e-30, 1.0])
+@pytest.mark.parametrize("shape", FORMS)
+def test_orthogonalize_zero_matrices(shape, eps):
+    """Zeros for any eps above zero, one whose inverse is no fp32 number included; their neighbours stay."""
+    nb, m, n = shape
+    G = _randn(_gen(m), nb, m, n, dtype=torch.float32)
+    G[0] = 0
+    out = orth(G, eps=eps)
+    assert (out[0] == 0).all()
+    if nb > 1:
+        assert errors(out[1:], newton64(G[1:], 5, eps=eps)) <= orth_tol(5)
