@@ -452,12 +452,15 @@ moe_status_t moe_combine_backward(const void* dout_dev, const void* y_perm_dev, 
  *           use). Calls that may run at the same time, captured graphs included,
  *           need a workspace each.
  * Any rows and cols in [1, 2^20], nb * (rows + 63) < 2^31. The state X is held in
- * two fp16 halves (22 bits, of a multiple near 1 where eps makes X small); the products take the upper half (scaled so that
- * |X|_2 about 1, which the norm and a polynomial with bounded steps give, fits)
- * and accumulate in fp32; matrices with at most 8 rows or columns are computed in
- * fp32. A polynomial that lets |X|_2 grow past some hundreds gives Inf or NaN. A
- * zero matrix gives zeros for eps > 0; NaN or Inf in one matrix do not reach
- * another. Nothing may overlap. */
+ * two fp16 halves (22 bits, of a multiple near 1 where eps makes X small). The
+ * products take the upper half, and A and b A + c A^2 in fp16, and accumulate in
+ * fp32; matrices with at most 8 rows or columns are computed in fp32. The fp16
+ * operands are scaled by up to sqrt(max(rows, cols)), so a step's result is right
+ * while |X|_2^2 and |b x^2 + c x^4| for every x in [0, |X|_2] stay below 65504 /
+ * sqrt(max(rows, cols)) at its start; past that it may be Inf or NaN. (At 4096 that is
+ * 1023: |X|_2 up to 32, with Muon's b and c up to 4.7; X starts at or below 1, and
+ * Muon's polynomial keeps it below 1.3.) A zero matrix gives zeros for eps > 0; NaN
+ * or Inf in one matrix do not reach another. Nothing may overlap. */
 moe_status_t moe_orthogonalize(const void* g_dev, int32_t nb, int32_t rows, int32_t cols,
                                moe_grad_type_t g_type, int32_t steps, float a, float b, float c,
                                float eps, float scale, void* out_dev, void* ws, size_t ws_bytes,

@@ -223,3 +223,21 @@ def test_orthogonalize_zero_matrices(shape, eps):
     assert (out[0] == 0).all()
     if nb > 1:
         assert errors(out[1:], newton64(G[1:], 5, eps=eps)) <= orth_tol(5)
+
+
+# ---------------------------------------------- polynomials at the end of the range
+@pytest.mark.parametrize("nb,p,q", [(1, 9, 9), (2, 40, 100), (1, 100, 2047), (1, 128, 4096), (1, 200, 4096), (1, 130, 16383),
+                                    (1, 300, 1 << 16), (20, 520, 1000), (3, 256, 16384)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_orthogonalize_up_to_its_range(nb, p, q, tall):
+    """Results are right up to the documented |X|_2 and polynomial, on a matrix whose one direction is an axis (its
+    square has no smaller elements) and on one of full rank."""
+    most = 65504 / math.sqrt(q)
+    axis = torch.zeros(nb, p, q, device="cuda")
+    axis[:, p // 2, q // 3] = 3.0
+    for G in (axis, _randn(_gen(q), nb, p, q, dtype=torch.float32)):
+        G = G.transpose(1, 2).contiguous() if tall else G
+        x = 0.999 * math.sqrt(most)  # |X|_2 after the first step, if it was 1
+        for steps, coeffs in ((2, (x - 0.9, 0.9, 0.0)), (1, (1.0, 0.0, 0.999 * most)), (1, (1.0, -0.999 * most, 0.0))):
+            err = errors(orth(G, steps=steps, coeffs=coeffs), newton64(G, steps, coeffs))
+            assert err <= orth_tol(steps), (steps, coeffs, err)
