@@ -15,7 +15,7 @@
 //     nothing else keeps the buffers apart. (Loads of the other CTAs' memory, stores
 //     to it and two cluster barriers took 10200 cycles a step instead of 6200.)
 //   - A^2 by MMA and B = b A + c A^2 in every CTA alike, over its own part of A;
-//   - B X by MMA, 128 columns at a time into two accumulators in turn, and
+//   - B X by MMA, the first and the last 128 columns each into an accumulator, and
 //     X <- a X + B X in place: a chunk's MMAs read that chunk's columns alone.
 // Bound by latency. Of a step's 12700 cycles (128 x 128 to a CTA, four CTAs) the
 // issue of the 24 MMAs takes 2500, the exchange of A 6200 (a third of it the copies'
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     ptx::tc_fence_after();
   };
   constexpr uint32_t kSquare = ptx::make_idesc(128, 128, 0, 0);
+  static_assert(kShortSlice == 2 * 128, "an accumulator of 128 columns for each chunk");
   const int chunks = (o.slice + 127) / 128;
   // The products, issued by thread 0. In the descriptors addresses count 16 bytes:
   // 16 k further is 2 along a K-major row, a block of 64 columns further 1024.
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     const uint64_t db = ptx::sw128_kmajor_desc(b_at), dx = ptx::sw128_mnmajor_desc(x_at + j * 32768, 16384);
 #pragma unroll 4
     for (int k = 0; k < ksteps; ++k)
-      ptx::mma_f16(tmem + (j & 1) * 128, db + (k >> 2) * 1024 + (k & 3) * 2, dx + k * 128, i, k > 0);
-    ptx::mma_commit(bar + 8 * (j & 1));
+      ptx::mma_f16(tmem + j * 128, db + (k >> 2) * 1024 + (k & 3) * 2, dx + k * 128, i, k > 0);
+    ptx::mma_commit(bar + 8 * j);
   };
 #pragma unroll 1
   for (int step = 0; step < o.steps; ++step) {
@@ -358,17 +359,17 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
     const float a_row = f.z * (o.a + rest[row]);
 #pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
-      wait(j & 1);
+      wait(j);
       if (used)
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          const int c0 = 128 * j + 64 * i + 32 * half, acc = (j & 1) * 128 + 64 * i + 32 * half;
+          const int c0 = 128 * j + 64 * i + 32 * half;  // of X and of the accumulators
           if (c0 >= o.slice) break;
           float v[32], x[32];
           uint32_t lo[16];
           __syncwarp();
           ptx::tmem_ld16(tmem + lanes + kShortLow + c0 / 2, lo);
-          load_acc32(tmem + lanes + acc, v);
+          load_acc32(tmem + lanes + c0, v);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint4 h = Warp::get(short_at(x_at, row, c0 / 8 + u));
@@ -406,11 +407,6 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
               if (col + k < o.q) dst[k * next] = __float2bfloat16_rn(r * v[k]);
           }
         }
-      if (j + 2 < chunks) {
-        hand_over();
-        if (tid == 0) issue_chunk(j + 2);
-        __syncwarp();
-      }
     }
   }
   // a wait that gave up: time for what is still on its way here
