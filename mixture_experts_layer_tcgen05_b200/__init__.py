@@ -169,7 +169,9 @@ def _ts(*args):
     """Addresses of dense tensors on the current device / ints / None: what a kernel there may read or write."""
     current, out = None, []
     for a in args:
-        if a is not None and a.__class__ is not int:
+        if a is not None and not isinstance(a, int):
+            if not hasattr(a, "get_device"):
+                raise TypeError(f"cannot take the address of {type(a)} on a device")
             device = a.get_device()
             if current is None and device >= 0:
                 current = _cuda_calls()[0]()
