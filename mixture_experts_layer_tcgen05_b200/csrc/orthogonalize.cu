@@ -85,7 +85,7 @@ __device__ __forceinline__ float2 join(uint32_t hi, uint32_t lo) {
 // kPart: a tile's sum over k is cut into `parts` ranges that run as tiles of
 // their own and leave their fp32 sums in [part, matrix, pp, pp]; sum_parts_kernel
 // adds them. One narrow matrix has too few tiles for the GPU otherwise (measured:
-// 7168 x 256, one tile, A in 43 us against 11 in 28 parts with their sum).
+// 7168 x 256, two 128 x 128 tiles a side: the update takes 175 us, 127 in 14 parts).
 enum SquareMode { kGram, kPart, kPoly };
 template <bool MN, SquareMode MODE, int SIDE>
 struct Square {
@@ -573,15 +573,13 @@ inline bool small_tiles(int64_t nb, int64_t mp, int64_t np) {
 inline int64_t square_tiles(int64_t pp, int64_t side) { return ceil_div(pp, side) * (ceil_div(pp, side) + 1) / 2; }
 
 // Parts that A's sum is cut into: as many as give every SM (pair) a tile, of at
-// least eight k blocks each (7168 x 256: 128 us in 14 parts, 136 in 28) and no more than the parts' buffer (at most as large
-// as the stack in fp32) holds; none for sums below 16 k blocks, which the launch
-// that adds the parts would not pay for (measured: 8 k blocks, one 512 x 128
-// before it had a form of its own, 134 us in parts, 129 without; 16 k blocks, 1024 x
-// 128, 133 and 139; 2048 x 256 158 and 182).
+// least eight k blocks each (7168 x 256: 128 us in 14 parts, 136 in 28), so none
+// below 16, which the launch that adds the parts would not pay for, and no more than
+// the parts' buffer (at most as large as the stack in fp32) holds. Measured, without
+// parts and with: 7168 x 256 175 and 127 us, 2048 x 256 (four parts) 111 and 109.
 inline int64_t units_of(int64_t pp, int64_t side) { return kSms / (side / 128) / square_tiles(pp, side); }
 inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
   const int64_t nkb = std::max(mp, np) / BK;
-  if (nkb < 16) return 1;
   const int64_t units = small_tiles(nb, mp, np) ? units_of(pp, 128) : units_of(pp, 256);
   return std::max<int64_t>(1, std::min({units / nb, nkb / 8, mp * np / (pp * pp)}));
 }

@@ -456,7 +456,8 @@ static int clusters_of_16() {
 }
 
 // The fewest CTAs that hold a matrix; more, down to slices of 128 columns, while
-// they all find an SM (eight 512 x 128: 47 us with slices of 128 or 64, 62 with 256).
+// they all find an SM (eight 512 x 128: 43 us with slices of 128, 54 with 256; sixteen
+// 44 and 54, and 79 with slices of 64, whose clusters do not all run at once).
 inline int short_cluster(int64_t stack, int64_t q) {
   int c = 1;
   while (c * kShortSlice < q) c *= 2;
