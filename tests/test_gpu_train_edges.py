@@ -241,3 +241,104 @@ def test_orthogonalize_up_to_its_range(nb, p, q, tall):
         for steps, coeffs in ((2, (x - 0.9, 0.9, 0.0)), (1, (1.0, 0.0, 0.999 * most)), (1, (1.0, -0.999 * most, 0.0))):
             err = errors(orth(G, steps=steps, coeffs=coeffs), newton64(G, steps, coeffs))
             assert err <= orth_tol(steps), (steps, coeffs, err)
+
+
+@pytest.mark.parametrize("shape", [(7, 72, 136), (4, 130, 260), (3, 301, 190), (20, 520, 700), (20, 700, 515), (3, 5, 600)])
+def test_orthogonalize_one_matrix_that_is_no_number(shape):
+    """NaN and Inf in one matrix, at its end and its start, reach no other; all of it is NaN."""
+    G = _randn(_gen(sum(shape)), *shape, dtype=torch.float32)
+    clean = orth(G).clone()
+    G[1, -1, -1], G[2, 0, 0] = math.nan, math.inf
+    out = torch.empty(shape, dtype=BF16, device="cuda")
+    ws = _ws(moe.moe_orthogonalize_workspace_size(*shape))
+    moe.moe_orthogonalize(G, *shape, moe.MOE_GRAD_F32, 5, COEFFS, 1e-7, 1.0, out, ws)
+    assert moe.moe_get_device_status(ws) == 0
+    rest = [i for i in range(shape[0]) if i not in (1, 2)]
+    assert torch.equal(out[rest], clean[rest])
+    assert torch.isnan(out[1]).all() and torch.isnan(out[2]).all()
+
+
+# ------------------------------------------------ elements past 2^31
+def test_row_gradient_past_32_bits():
+    """Rows whose results start past 2^31 elements: the last expert's against the formula, the first's too."""
+    E, N, K, R = 2, 128, 4096, 530_000  # dA: 2.17e9 elements, with the gate 4.3e9
+    gen = _gen(91)
+    dC, B = _randn(gen, R, N), _randn(gen, E, N, K, std=0.05)
+    off = torch.tensor([0, 300_000, R], dtype=torch.int32, device="cuda")
+    probe = torch.tensor([0, 1, 299_999, 300_000, 524_287, 524_288, 529_000, R - 1], device="cuda")
+    owner = (probe >= 300_000).long()
+    d = torch.einsum("rn,rnk->rk", dC[probe].double(), B[owner].double())
+    eps = torch.einsum("rn,rnk->rk", dC[probe].double().abs(), B[owner].double().abs()) * N * 2.0**-23
+    out, ws = torch.empty(R, K, dtype=BF16, device="cuda"), _ws(256)
+    moe.moe_grouped_gemm_dgrad(dC, B, off, R, E, N, K, moe.MOE_EPILOGUE_NONE, out, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    assert ((out[probe].double() - d).abs() <= d.abs() * 2.0**-8 + eps).all()
+    del out
+    gu = torch.empty(R, 2 * K, dtype=BF16, device="cuda")
+    gu[:, :K], gu[:, K:] = 1.5, -0.75
+    out, h = torch.empty(R, 2 * K, dtype=BF16, device="cuda"), torch.empty(R, K, dtype=BF16, device="cuda")
+    moe.moe_grouped_gemm_dgrad(dC, B, off, R, E, N, K, moe.MOE_EPILOGUE_REGLU, out, gu=gu, h=h, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    for got, f in ((out[probe, :K], -0.75), (out[probe, K:], 1.5)):
+        assert ((got.double() - f * d).abs() <= (f * d).abs() * 2.0**-8 + abs(f) * eps).all()
+    assert (h == -1.125).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "add"])
+def test_weight_gradient_past_32_bits(kind):
+    E, N, K, each = 40, 8192, 8192, 19  # 2.7e9 elements
+    R = E * each
+    gen = _gen(92)
+    dC, A = _randn(gen, R, N), _randn(gen, R, K)
+    off = (torch.arange(E + 1, device="cuda") * each).to(torch.int32)
+    out = torch.ones(E, N, K, dtype=BF16 if kind == "bf16" else torch.float32, device="cuda")
+    ws = _ws(256)
+    moe.moe_grouped_gemm_wgrad(dC, A, off, R, E, N, K, moe.MOE_GRAD_BF16 if kind == "bf16" else moe.MOE_GRAD_F32,
+                               kind == "add", out, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    for e in (0, 31, 32, E - 1):  # 2^31 elements end with the 32nd expert
+        x, y = dC[e * each:(e + 1) * each].double(), A[e * each:(e + 1) * each].double()
+        for rows in (slice(0, 64), slice(N - 64, N)):
+            ref, tol = x[:, rows].T @ y, (x[:, rows].abs().T @ y.abs()) * each * 2.0**-23
+            ref = ref + (kind == "add")
+            assert ((out[e, rows].double() - ref).abs() <= ref.abs() * (2.0**-8 if kind == "bf16" else 2.0**-24) + tol).all()
+
+
+def test_combine_gradient_past_32_bits():
+    T, H, k = 40_000, 7168, 8  # 2.3e9 elements of y
+    gen = _gen(93)
+    R = T * k
+    dout = _randn(gen, T, H)
+    y = torch.empty(R, H, dtype=BF16, device="cuda")
+    y.copy_(torch.arange(1, R + 1, device="cuda")[:, None].remainder(251).expand(R, H))
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    inv = torch.randperm(R, generator=gen, device="cuda").to(torch.int32).view(T, k)
+    dw, ws = torch.empty(T, k, device="cuda"), _ws(256)
+    factor = y[inv.long().view(-1), 0].double().view(T, k)
+    moe.moe_combine_backward(dout, y, w, inv, (T, H, 128, 8, k), y, dw, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    total, size = dout.double().sum(1, keepdim=True), dout.double().abs().sum(1, keepdim=True)
+    assert ((dw.double() - factor * total).abs() <= factor * size * H * 2.0**-24).all()
+    for t in (0, 1, T // 2, T - 1):
+        ref = w[t, :, None].double() * dout[t].double()
+        assert ((y[inv[t].long()].double() - ref).abs() <= ref.abs() * (2.0**-8 + 2.0**-23)).all()
+    last = inv.view(-1).argmax()  # the row at the end of y
+    ref = w.view(-1)[last].double() * dout[last // k].double()
+    assert ((y[R - 1].double() - ref).abs() <= ref.abs() * (2.0**-8 + 2.0**-23)).all()
+
+
+@pytest.mark.parametrize("nb,rows,cols,hold", [(70_000, 128, 256, 70_000), (9000, 512, 512, 9000), (9000, 512, 512, 3000),
+                                               (70_000, 8, 4096, 20_000)])
+def test_update_past_32_bits(nb, rows, cols, hold):
+    """Stacks of more than 2^31 elements and of more matrices than a grid's second axis counts."""
+    one = _randn(_gen(94), 7, rows, cols, dtype=torch.float32)
+    G = torch.empty(nb, rows, cols, dtype=BF16, device="cuda")
+    for i in range(7):
+        G[i::7] = one[i].to(BF16)
+    out = torch.empty_like(G)
+    ws = _ws(moe.moe_orthogonalize_workspace_size(hold, rows, cols))
+    moe.moe_orthogonalize(G, nb, rows, cols, moe.MOE_GRAD_BF16, 3, COEFFS, 1e-7, 1.0, out, ws)
+    assert moe.moe_get_device_status(ws) == 0
+    assert errors(out[:7], newton64(G[:7], 3)) <= orth_tol(3)
+    for i in range(7):
+        assert torch.equal(out[i::7], out[i].expand(len(range(i, nb, 7)), rows, cols))
