@@ -1,6 +1,9 @@
 """The training operators at the edges of what they document, against the formulas
 in 64 bits. Tolerances count roundings as in test_gpu_train.py."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -342,3 +345,44 @@ def test_update_past_32_bits(nb, rows, cols, hold):
     assert errors(out[:7], newton64(G[:7], 3)) <= orth_tol(3)
     for i in range(7):
         assert torch.equal(out[i::7], out[i].expand(len(range(i, nb, 7)), rows, cols))
+
+
+# ------------------------------------------------------- the first call of a process
+FIRST = """
+import sys, torch
+sys.path[:0] = [{root!r}, {tests!r}]
+import mixture_experts_layer_tcgen05_b200 as moe
+import test_gpu_train_edges as t
+G = t._randn(t._gen(5), *{shape}, dtype=torch.float32)
+out = torch.empty({shape}, dtype=torch.bfloat16, device="cuda")
+ws = t._ws(moe.moe_orthogonalize_workspace_size(*{shape}))
+R, N, K = 3000, 256, 128
+dC, A, B, gu = t._randn(t._gen(6), R, N), t._randn(t._gen(7), R, K), t._randn(t._gen(8), 1, N, K), t._randn(t._gen(9), R, 2 * K)
+off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+dA, dB, gws = torch.empty(R, 2 * K, dtype=torch.bfloat16, device="cuda"), torch.empty(1, N, K, device="cuda"), t._ws(1 << 24)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def calls():
+    moe.moe_orthogonalize(G, *{shape}, moe.MOE_GRAD_F32, 5, t.COEFFS, 1e-7, 1.0, out, ws)
+    moe.moe_grouped_gemm_dgrad(dC, B, off, R, 1, N, K, moe.MOE_EPILOGUE_SWIGLU, dA, gu=gu, ws=gws)
+    moe.moe_grouped_gemm_wgrad(dC, A, off, R, 1, N, K, moe.MOE_GRAD_F32, 0, dB, ws=gws)
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (out, dA, dB)]
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (out, dA, dB)))
+assert moe.moe_get_device_status(ws) == 0 and moe.moe_get_device_status(gws) == 0
+assert t.errors(out, t.newton64(G, 5)) <= t.orth_tol(5)
+"""
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 3000), (2, 128, 512), (1, 128, 4096), (1, 300, 200), (20, 520, 700)])
+def test_first_call_of_a_process_is_captured(shape):
+    """Kernels' attributes and the occupancy that a rule asks for are set while a stream is being captured."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests, shape=shape)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
