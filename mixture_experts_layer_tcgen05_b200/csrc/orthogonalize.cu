@@ -594,7 +594,8 @@ inline int64_t gram_parts(int64_t nb, int64_t mp, int64_t np, int64_t pp) {
 // sums y y^T, the next step's A; the cluster's blocks read each other's sums and
 // add them in the same order. Bound by the latency of a pass's loads.
 // Measured, against the MMA tiles: 4 x 4096 17 and 99 us, 16384 x 8 59 and 141,
-// 300 of 400 x 8 64 and 262, 8 x 300000 678 and 631.
+// 300 of 400 x 8 64 and 262, 8 x 300000 678 and 631: one matrix has eight SMs here
+// however long it is; one that long takes this form for its precision.
 constexpr int kNarrow = 8, kNarrowThreads = 512, kNarrowCluster = 8;
 inline bool narrow(int64_t rows, int64_t cols) { return std::min(rows, cols) <= kNarrow; }
 

@@ -21,8 +21,8 @@
 // issue of the 24 MMAs takes 2500, the exchange of A 6200 (a third of it the copies'
 // bytes, 48 KB each way) and the epilogues 3700; before the first step 10000 go to
 // reading G and its norm. Measured, against the launches of the general form: eight
-// 512 x 128 43 and 84 us, one 128 x 128 28 and 74, 16 x 512 25 and 67, 100 x 2000 57
-// and 95, a thousand 128 x 128 199 and 648, 64 of 2048 x 128 316 and 339. A CTA's
+// 512 x 128 43 and 84 us, one 128 x 128 27 and 74, 16 x 512 25 and 67, 100 x 2000 55
+// and 95, a thousand 128 x 128 199 and 648, 64 of 2048 x 128 312 and 339. A CTA's
 // slice is at most the 256 columns that shared memory has room for beside the parts of
 // A; the rest is the general form's.
 #pragma once
@@ -465,7 +465,7 @@ inline int short_cluster(int64_t stack, int64_t q) {
   return c;
 }
 // Sides past eight slices take clusters of 16, of which few run at a time: only
-// stacks that run at once (128 x 4096: one 65 us, 100 in the general form; 16 of them
+// stacks that run at once (128 x 4096: one 63 us, 100 in the general form; 16 of them
 // 192 and 240, but 64 of 64 x 4096 565 and 381, 128 of 128 x 2500 1989 and 808).
 inline bool is_short(int64_t stack, int64_t rows, int64_t cols) {
   const int64_t q = std::max(rows, cols);
