@@ -460,8 +460,10 @@ moe_status_t moe_combine_backward(const void* dout_dev, const void* y_perm_dev, 
  * while |X|_2^2 and |b x^2 + c x^4| for every x in [0, |X|_2] stay below 65504 /
  * sqrt(max(rows, cols)) at its start; past that it may be Inf or NaN. (At 4096 that is
  * 1023: |X|_2 up to 32, with Muon's b and c up to 4.7; X starts at or below 1, and
- * Muon's polynomial keeps it below 1.3.) A zero matrix gives zeros for eps > 0; NaN
- * or Inf in one matrix do not reach another. Nothing may overlap. */
+ * Muon's polynomial keeps it below 1.3.) fp16's lower end counts beside a X: a
+ * polynomial with |a| below 1/2, whose X dwindles or is b A + c A^2 times X alone, loses
+ * bits. A zero matrix gives zeros for eps > 0; NaN or Inf in one matrix do not reach
+ * another. Nothing may overlap. */
 moe_status_t moe_orthogonalize(const void* g_dev, int32_t nb, int32_t rows, int32_t cols,
                                moe_grad_type_t g_type, int32_t steps, float a, float b, float c,
                                float eps, float scale, void* out_dev, void* ws, size_t ws_bytes,

@@ -386,3 +386,14 @@ def test_first_call_of_a_process_is_captured(shape):
     code = FIRST.format(root=os.path.dirname(tests), tests=tests, shape=shape)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("coeffs,steps,eps", [((0.5, 0.25, 0.0), 5, 1e5), ((1.0, 1e4, 1e8), 2, 1e6), ((2.0, -1e3, 0.0), 1, 1e5),
+                                              ((1.0, -1e12, 0.0), 1, 1e9), ((1e20, 0.0, 0.0), 1, 1e20),
+                                              ((-1e20, 1.0, 0.0), 2, 1e38)])
+@pytest.mark.parametrize("shape", [(2, 4, 100), (2, 40, 72), (1, 300, 130), (2, 130, 260), (20, 520, 700), (20, 700, 515)])
+def test_orthogonalize_small_x_under_large_coefficients(shape, coeffs, steps, eps):
+    """A polynomial whose coefficients are large while b A + c A^2 is not, on an X that eps makes small."""
+    G = _randn(_gen(steps), *shape, dtype=torch.float32)
+    err = errors(orth(G, steps=steps, coeffs=coeffs, eps=eps), newton64(G, steps, coeffs, eps))
+    assert err <= orth_tol(steps), err
