@@ -399,8 +399,9 @@ typedef enum { MOE_GRAD_BF16 = 0, MOE_GRAD_F32 = 1 } moe_grad_type_t;
  *   h_dev  bf16 [M_total, K] or NULL (gated), else NULL
  * N, K multiples of 128 up to 2^24, E*N < 2^31. Accumulation is the tensor cores'
  * fp32 (cut off, not rounded, every 16 terms: the sum is off by about 2e-5 of itself
- * after N = 16384, in proportion); every output is rounded once. Offsets are clamped to [0, M_total]; rows of no expert
- * are left as they were. Outputs overlap neither inputs nor each other.
+ * after N = 16384, in proportion); every output is rounded once. Offsets are clamped
+ * to [0, M_total]; rows of no expert are left as they were. Outputs overlap neither
+ * inputs nor each other.
  *   ws: its first 256 bytes hold the status word (zero before the first use),
  *       the rest may take fp32 partial sums of long sums over few tiles; the sum's
  *       order, and so its last bits, depend on how many fit. Inputs and outputs
