@@ -80,6 +80,13 @@ __device__ __forceinline__ float2 join(uint32_t hi, uint32_t lo) {
   return make_float2(fmaf(l.x, 1.0f / 2048.0f, h.x), fmaf(l.y, 1.0f / 2048.0f, h.y));
 }
 
+// A bf16 of G. cuda_bf16.h's __ldg is an asm without volatile, which the compiler may
+// move ahead of the check that its address is inside. (It did: narrow_kernel's idle
+// threads read past the end of a small G, which faults where nothing is mapped.)
+__device__ __forceinline__ float ldg_bf16(const void* g, int64_t i) {
+  return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(g) + i) << 16);
+}
+
 // The products of X with itself (kGram, kPart) or of A with itself (kPoly):
 // symmetric results, tiles on and above the diagonal.
 // kPart: a tile's sum over k is cut into `parts` ranges that run as tiles of
@@ -629,8 +636,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = rank * kNarrowThreads + threadIdx.x;
   auto load = [&](int r, int j) {
     const int64_t i = at + r * sp + j * sq;
-    return g_f32 ? __ldg(static_cast<const float*>(g) + i)
-                 : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(g) + i));
+    return g_f32 ? __ldg(static_cast<const float*>(g) + i) : ldg_bf16(g, i);
   };
   // another block's shared memory, read between two cluster barriers
   auto peer_f32 = [](const float* v, int r) {

@@ -132,10 +132,9 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_kernel(ShortArgs o) {
       for (int j = 0; j < 32; ++j)
         if (col + j < o.q) v[j] = __ldg(src + j * step);
     } else {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(o.g) + base;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (col + j < o.q) v[j] = __bfloat162float(__ldg(src + j * step));
+        if (col + j < o.q) v[j] = ldg_bf16(o.g, base + j * step);
     }
   };
   // 32 columns of the state from local column c0: two halves, 16 words each
