@@ -329,6 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.step();
       }
     }
+    // The leading CTA frees the other one's stages, too: all of it has come before that
+    // one goes. (A stage that was never used is free.)
+    if (CG == 2 && loader && rank != 0 && ok) {
+      for (int i = 0; i < STAGES; ++i, at.step()) ptx::mbar_wait(empty0 + at.bar, at.parity ^ 1, status, kSiteDrain);
+    }
     // every load of the ring has landed before this CTA (for a pair: both) goes
     if (loader && rank == 0) {
       for (uint32_t b = 0; b < STAGES * 8; b += 8) {
@@ -510,6 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // the last commit reaches both CTAs: the one that issued it has waited for it
+  if (CG == 2 && rank != 0 && warp == 1) ptx::mbar_wait(drain, 0, status, kSiteDrain);
   if constexpr (CG == 2) ptx::cluster_sync();  // no CTA leaves while the other may still signal or read it
   if (warp == 1) {
     ptx::tc_fence_after();
